@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_ABI_VERSION 5
+#define NVFP4_ABI_VERSION 6
 
 /* Status codes. All argument validation happens before any HIP call. */
 typedef enum nvfp4_status {
@@ -252,6 +252,101 @@ int nvfp4_mxfp8_quantize_elem(const void* x_bf16, int64_t M, int64_t K, int elem
 int nvfp4_mxfp8_gemm_elem(const void* a_codes, const void* a_scales, int a_element,
                           const void* w_codes, const void* w_scales, int w_element, int64_t M,
                           int64_t N, int64_t K, void* out_bf16, void* stream);
+
+/*
+ * MXFP4 (OCP microscaling) path: the 4-bit member of the same family, which gfx950's
+ * block-scaled MFMA multiplies as stored, at twice its fp8 rate.
+ *   - elements are E2M1 codes, packed as in NVFP4 (uint8 [rows, K/2], element 2j in the
+ *     low nibble of byte j); each 32-element block along K shares an E8M0 scale byte
+ *     (value 2^(byte - 127)), uint8 [rows, K/32];
+ *   - quantization: e = floor(log2(amax)) - 2 clamped to [-127, 127] (all-zero block:
+ *     byte 0); element = the E2M1 value nearest to x / 2^e, ties to the even code,
+ *     saturating at 6, sign copied. A block that holds a NaN or an infinity takes byte
+ *     0xFF (the scale format's NaN) and codes 0: every element reads back as NaN;
+ *   - GEMM: out = bf16_RNE(sum_k a_k w_k) with the decoded values; any result within
+ *     2^-10 * sum_k |a_k w_k| + 1 bf16 ulp of the exact value is correct and the library's
+ *     result is deterministic for a given shape. A 0xFF scale byte makes its row's
+ *     results NaN.
+ *
+ * nvfp4_mxfp4_quantize: x_bf16 [M, K] (16-byte aligned) -> packed uint8 [M, K/2] (16-byte
+ * aligned) and scales uint8 [M, K/32] (4-byte aligned). K % 32 == 0. Bit-exact to the rule
+ * above. x need not be finite.
+ */
+int nvfp4_mxfp4_quantize(const void* x_bf16, int64_t M, int64_t K, void* packed, void* scales,
+                         void* stream);
+
+/*
+ * nvfp4_mxfp4_dequantize: the stored values as bf16 [M, K] (16-byte aligned). Exact, except
+ * that a value of 2^128 or more (scale bytes 253 and 254 with the largest codes) becomes an
+ * infinity. Arguments as in nvfp4_mxfp4_quantize.
+ */
+int nvfp4_mxfp4_dequantize(const void* packed, const void* scales, int64_t M, int64_t K,
+                           void* out_bf16, void* stream);
+
+/*
+ * nvfp4_mxfp4_gemm: out_bf16 [M, N] = A_hat [M, K] W_hat [N, K]^T with both operands MXFP4.
+ * K % 32 == 0, K <= 2^22, M and N at most 2^31 - 1 (else NVFP4_ERROR_INVALID_SHAPE);
+ * packed operands and out 16-byte aligned, scales 4-byte aligned.
+ */
+int nvfp4_mxfp4_gemm(const void* a_packed, const void* a_scales, const void* w_packed,
+                     const void* w_scales, int64_t M, int64_t N, int64_t K, void* out_bf16,
+                     void* stream);
+
+/* Workspace bytes nvfp4_mxfp4_linear needs for an [M, K] activation (packed and scales,
+ * each rounded up to 256 bytes). Returns 0 for shapes the linear rejects. */
+size_t nvfp4_mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
+
+/*
+ * nvfp4_mxfp4_linear: nvfp4_mxfp4_quantize of x into the workspace, then
+ * nvfp4_mxfp4_gemm, both on `stream`. The workspace (16-byte aligned, at least
+ * nvfp4_mxfp4_linear_workspace_bytes(M, K) bytes) holds the quantized activations on
+ * return: packed [M, K/2] at offset 0, scales [M, K/32] at round_up(M*K/2, 256). Calls that
+ * may overlap in time need workspaces of their own.
+ */
+int nvfp4_mxfp4_linear(const void* x_bf16, const void* w_packed, const void* w_scales, int64_t M,
+                       int64_t N, int64_t K, void* out_bf16, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Mixture-of-experts layer for a few tokens (decode batches), MXFP4 expert weights and bf16
+ * activations.
+ *
+ * nvfp4_moe_router: logits[t, e] = RN32(sum_h x[t, h] w[e, h]), summed in fp64.
+ *   x_bf16 [T, H], router_bf16 [E, H] (16-byte aligned), logits fp32 [T, E] (4-byte aligned);
+ *   H % 32 == 0, E in [1, 512], T at most 2^21.
+ */
+int nvfp4_moe_router(const void* x_bf16, const void* router_bf16, int64_t T, int64_t E, int64_t H,
+                     void* logits, void* stream);
+
+/*
+ * nvfp4_mxfp4_moe: the routed experts' gated feed-forward.
+ *   routing: each token takes the top_k experts of largest logit, ties to the lowest index.
+ *     A logit of -inf is never chosen; a token with fewer than top_k others fills up with
+ *     id -1 and weight 0, and a token with none has output 0 (how a caller marks padding).
+ *     weight = softmax of the logits at the chosen expert, over all E (renormalize == 0) or
+ *     over the chosen ones (renormalize == 1). A NaN logit ranks first; it, or a logit of
+ *     +inf, makes that token's weights and output NaN.
+ *   expert e: h = silu(Wg x) * (Wu x), rounded to bf16; y = W2 h. Gate rows Wg are rows
+ *     0..I-1 of W13 [E, 2I, H], up rows Wu rows I..2I-1; W2 is [E, H, I].
+ *   out[t] = bf16_RNE(sum_j weight_tj y_tj), sums in fp32. Weights decode exactly; a value of
+ *     2^128 or more reads as an infinity, a 0xFF scale byte as NaN.
+ *   x_bf16 [T, H], logits fp32 [T, E]; w13_packed [E, 2I, H/2], w13_scales [E, 2I, H/32],
+ *   w2_packed [E, H, I/2], w2_scales [E, H, I/32]; out_bf16 [T, H]; topk_ids int32 [T, top_k]
+ *   and topk_weights fp32 [T, top_k] are written when not null.
+ *   H and I multiples of 32, at most 2^20; E in [1, 512]; top_k in [1, min(E, 16)]; T at most
+ *   2^21 (else NVFP4_ERROR_INVALID_SHAPE). x, packed weights, out and workspace 16-byte
+ *   aligned, scales, logits, topk_ids and topk_weights 4-byte aligned.
+ *   The workspace holds at least nvfp4_mxfp4_moe_workspace_bytes(T, E, I, top_k) bytes. Calls
+ *   that may overlap in time need workspaces of their own. The result is deterministic for
+ *   given arguments. Tokens are taken in groups of 64 that read their experts' weights each
+ *   for itself: for long prompts, sort tokens by expert and use nvfp4_mxfp4_gemm.
+ */
+size_t nvfp4_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k);
+int nvfp4_mxfp4_moe(const void* x_bf16, const void* logits, const void* w13_packed,
+                    const void* w13_scales, const void* w2_packed, const void* w2_scales,
+                    int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k, int renormalize,
+                    void* out_bf16, void* topk_ids, void* topk_weights, void* workspace,
+                    size_t workspace_bytes, void* stream);
 
 /*
  * Rowwise FP8 ("fp8r") path: the other scheme of the "BFL (fp8r / nvfp4)" page (scheme

@@ -10,6 +10,10 @@ Python entry points (thin wrappers over the C ABI in include/nvfp4.h):
 * :func:`linear_plan` -- whether :func:`linear` runs a shape as one fused kernel
 * :func:`gemm_w4a16` -- NVFP4 weights x bf16 activations (not quantized), bf16 output
 * :func:`mxfp8_quantize`, :func:`mxfp8_gemm` -- the MXFP8 (OCP microscaling) path
+* :func:`mxfp4_quantize`, :func:`mxfp4_dequantize`, :func:`mxfp4_gemm`,
+  :func:`mxfp4_linear` -- the MXFP4 (OCP microscaling) path
+* :func:`moe_router`, :func:`mxfp4_moe` -- a mixture-of-experts layer for a few tokens, its
+  experts' weights in MXFP4
 * :func:`fp8r_quantize`, :func:`fp8r_gemm` -- the rowwise FP8 path
 * :func:`amax`, :func:`calibrate`, :func:`global_scale_from_amax` -- global scales
 * :func:`calibrate_device` -- a global scale kept on the device (quantize, gemm and
@@ -30,6 +34,14 @@ from .ops import (  # noqa: F401
     linear,
     linear_plan,
     linear_workspace_bytes,
+    moe_router,
+    mxfp4_dequantize,
+    mxfp4_gemm,
+    mxfp4_linear,
+    mxfp4_linear_workspace_bytes,
+    mxfp4_moe,
+    mxfp4_moe_workspace_bytes,
+    mxfp4_quantize,
     mxfp8_gemm,
     mxfp8_quantize,
     quantize,

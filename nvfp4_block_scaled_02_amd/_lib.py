@@ -11,7 +11,7 @@ import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libnvfp4.so")
-ABI_VERSION = 5
+ABI_VERSION = 6
 
 STATUS = {
     0: "NVFP4_SUCCESS",
@@ -47,6 +47,15 @@ SIGNATURES = {
     "nvfp4_mxfp8_gemm_elem": (_int, [_vp, _vp, _int, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp]),
     "nvfp4_fp8r_quantize": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "nvfp4_fp8r_gemm": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "nvfp4_mxfp4_quantize": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "nvfp4_mxfp4_dequantize": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
+    "nvfp4_mxfp4_gemm": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "nvfp4_mxfp4_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "nvfp4_mxfp4_linear": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, ctypes.c_size_t, _vp]),
+    "nvfp4_moe_router": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "nvfp4_mxfp4_moe_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _i64]),
+    "nvfp4_mxfp4_moe": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int,
+                               _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "nvfp4_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "nvfp4_linear": (_int, [_vp, _f32, _vp, _vp, _f32, _i64, _i64, _i64, _vp, _vp,
                             ctypes.c_size_t, _vp]),

@@ -133,6 +133,47 @@ int check_w4a16_shape(int64_t M, int64_t N, int64_t K) {
   return NVFP4_SUCCESS;
 }
 
+// Shape rules of one MXFP4 tensor and of nvfp4_mxfp4_gemm / _linear.
+int check_mx4_rows(int64_t rows, int64_t K) {
+  const int s = check_shape(rows, K);
+  return s ? s : K % 32 != 0 ? (int)NVFP4_ERROR_INVALID_SHAPE : (int)NVFP4_SUCCESS;
+}
+int check_mx4_shape(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || M > 0x7FFFFFFF || N > 0x7FFFFFFF || K < 32 || K % 32 != 0 ||
+      K > ((int64_t)1 << 22))
+    return NVFP4_ERROR_INVALID_SHAPE;
+  return NVFP4_SUCCESS;
+}
+int validate_mx4_gemm(const void* ap, const void* as, const void* wp, const void* ws, int64_t M,
+                      int64_t N, int64_t K, const void* out) {
+  if (!ap || !as || !wp || !ws || !out) return NVFP4_ERROR_INVALID_VALUE;
+  const int s = check_mx4_shape(M, N, K);
+  if (s) return s;
+  if (!aligned(ap, 16) || !aligned(wp, 16) || !aligned(out, 16) || !aligned(as, 4) ||
+      !aligned(ws, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  return NVFP4_SUCCESS;
+}
+
+// Sizes of the mixture-of-experts calls: tokens, experts and one width (H or I).
+bool moe_sizes(int64_t T, int64_t E, int64_t width) {
+  return T >= 0 && T <= nvfp4::kMoeMaxTokens && E >= 1 && E <= nvfp4::kMoeMaxExperts &&
+         width >= 32 && width % 32 == 0 && width <= ((int64_t)1 << 20);
+}
+struct MoeWorkspace {
+  size_t ids, weights, plan, h, bytes;  // offsets, and the whole
+};
+MoeWorkspace moe_workspace(int64_t T, int64_t I, int64_t top_k) {
+  const size_t slots = (size_t)(T * top_k);
+  MoeWorkspace w;
+  w.ids = 0;
+  w.weights = w.ids + round_up(slots * 4, 256);
+  w.plan = w.weights + round_up(slots * 4, 256);
+  w.h = w.plan + round_up((size_t)nvfp4::moe_plan_bytes(T), 256);
+  w.bytes = w.h + round_up(slots * (size_t)I * 2, 256);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -323,6 +364,133 @@ int nvfp4_fp8r_gemm(const void* ac, const void* as, const void* wc, const void* 
   nvfp4::GemmProblem p{(const uint8_t*)ac, (const uint8_t*)as, (const uint8_t*)wc,
                        (const uint8_t*)ws, (uint16_t*)out, M, N, K, 1.0f};
   hipError_t e = nvfp4::launch_fp8r_gemm(p, (hipStream_t)stream, info);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+// ---- MXFP4 -------------------------------------------------------------------------------
+
+int nvfp4_mxfp4_quantize(const void* x, int64_t M, int64_t K, void* packed, void* scales,
+                         void* stream) {
+  if (!x || !packed || !scales) return NVFP4_ERROR_INVALID_VALUE;
+  int s = check_mx4_rows(M, K);
+  if (s) return s;
+  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, 4)) return NVFP4_ERROR_MISALIGNED;
+  if (M == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  s = current_device(&info);
+  if (s) return s;
+  hipError_t e = nvfp4::launch_mx4_quantize(x, M, K, packed, scales, (hipStream_t)stream, info);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+int nvfp4_mxfp4_dequantize(const void* packed, const void* scales, int64_t M, int64_t K, void* out,
+                           void* stream) {
+  if (!packed || !scales || !out) return NVFP4_ERROR_INVALID_VALUE;
+  int s = check_mx4_rows(M, K);
+  if (s) return s;
+  if (!aligned(packed, 16) || !aligned(out, 16) || !aligned(scales, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  if (M == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  s = current_device(&info);
+  if (s) return s;
+  hipError_t e = nvfp4::launch_mx4_dequantize(packed, scales, M, K, out, (hipStream_t)stream, info);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+int nvfp4_mxfp4_gemm(const void* ap, const void* as, const void* wp, const void* ws, int64_t M,
+                     int64_t N, int64_t K, void* out, void* stream) {
+  int s = validate_mx4_gemm(ap, as, wp, ws, M, N, K, out);
+  if (s) return s;
+  if (M == 0 || N == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  s = current_device(&info);
+  if (s) return s;
+  nvfp4::GemmProblem p{(const uint8_t*)ap, (const uint8_t*)as, (const uint8_t*)wp,
+                       (const uint8_t*)ws, (uint16_t*)out, M, N, K, 1.0f, nullptr, nullptr};
+  hipError_t e = nvfp4::launch_mx4_gemm(p, (hipStream_t)stream, info);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+size_t nvfp4_mxfp4_linear_workspace_bytes(int64_t M, int64_t K) {
+  if (check_mx4_shape(M, 0, K)) return 0;
+  return round_up((size_t)(M * (K / 2)), 256) + round_up((size_t)(M * (K / 32)), 256);
+}
+
+int nvfp4_mxfp4_linear(const void* x, const void* wp, const void* ws, int64_t M, int64_t N,
+                       int64_t K, void* out, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (!x || !workspace) return NVFP4_ERROR_INVALID_VALUE;
+  int s = check_mx4_shape(M, N, K);
+  if (s) return s;
+  uint8_t* ap = (uint8_t*)workspace;
+  uint8_t* as = ap + round_up((size_t)(M * (K / 2)), 256);
+  s = validate_mx4_gemm(ap, as, wp, ws, M, N, K, out);
+  if (s) return s;
+  if (!aligned(x, 16)) return NVFP4_ERROR_MISALIGNED;
+  if (workspace_bytes < nvfp4_mxfp4_linear_workspace_bytes(M, K)) return NVFP4_ERROR_WORKSPACE;
+  if (M == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  s = current_device(&info);
+  if (s) return s;
+  hipError_t e = nvfp4::launch_mx4_quantize(x, M, K, ap, as, (hipStream_t)stream, info);
+  if (e != hipSuccess) return hip_fail(e);
+  if (N == 0) return NVFP4_SUCCESS;
+  nvfp4::GemmProblem p{ap, as, (const uint8_t*)wp, (const uint8_t*)ws, (uint16_t*)out, M, N, K,
+                       1.0f, nullptr, nullptr};
+  e = nvfp4::launch_mx4_gemm(p, (hipStream_t)stream, info);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+// ---- mixture of experts ------------------------------------------------------------------
+
+int nvfp4_moe_router(const void* x, const void* w, int64_t T, int64_t E, int64_t H, void* logits,
+                     void* stream) {
+  if (!x || !w || !logits) return NVFP4_ERROR_INVALID_VALUE;
+  if (!moe_sizes(T, E, H)) return NVFP4_ERROR_INVALID_SHAPE;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(logits, 4)) return NVFP4_ERROR_MISALIGNED;
+  if (T == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  int s = current_device(&info);
+  if (s) return s;
+  hipError_t e = nvfp4::launch_moe_router(x, w, T, E, H, logits, (hipStream_t)stream);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+size_t nvfp4_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k) {
+  if (!moe_sizes(T, E, I) || top_k < 1 || top_k > E || top_k > nvfp4::kMoeMaxTopK) return 0;
+  const MoeWorkspace w = moe_workspace(T, I, top_k);
+  return w.bytes;
+}
+
+int nvfp4_mxfp4_moe(const void* x, const void* logits, const void* w13p, const void* w13s,
+                    const void* w2p, const void* w2s, int64_t T, int64_t E, int64_t H, int64_t I,
+                    int64_t top_k, int renormalize, void* out, void* topk_ids, void* topk_weights,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x || !logits || !w13p || !w13s || !w2p || !w2s || !out || !workspace)
+    return NVFP4_ERROR_INVALID_VALUE;
+  if (renormalize != 0 && renormalize != 1) return NVFP4_ERROR_INVALID_VALUE;
+  if (!moe_sizes(T, E, H) || !moe_sizes(T, E, I) || top_k < 1 || top_k > E ||
+      top_k > nvfp4::kMoeMaxTopK)
+    return NVFP4_ERROR_INVALID_SHAPE;
+  if (!aligned(x, 16) || !aligned(w13p, 16) || !aligned(w2p, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 16) || !aligned(logits, 4) || !aligned(w13s, 4) || !aligned(w2s, 4) ||
+      !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  const MoeWorkspace w = moe_workspace(T, I, top_k);
+  if (workspace_bytes < w.bytes) return NVFP4_ERROR_WORKSPACE;
+  if (T == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  int s = current_device(&info);
+  if (s) return s;
+  uint8_t* base = (uint8_t*)workspace;
+  nvfp4::MoeProblem p{(const uint16_t*)x, (const float*)logits, (const uint8_t*)w13p,
+                      (const uint8_t*)w13s, (const uint8_t*)w2p, (const uint8_t*)w2s,
+                      (uint16_t*)out, topk_ids ? (int*)topk_ids : (int*)(base + w.ids),
+                      topk_weights ? (float*)topk_weights : (float*)(base + w.weights),
+                      base + w.plan, (uint16_t*)(base + w.h), T, H, I, (int)E, (int)top_k,
+                      renormalize == 1};
+  hipError_t e = nvfp4::launch_moe(p, (hipStream_t)stream);
   return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
 }
 

@@ -132,6 +132,37 @@ hipError_t launch_mx_selftest_e4m3_exhaustive(unsigned long long* count, uint32_
 hipError_t launch_mx_selftest_e5m2_exhaustive(unsigned long long* count, uint32_t* first,
                                               hipStream_t stream);
 
+// MXFP4: packed codes and E8M0 scale bytes in GemmProblem's a_packed/a_scales/w_packed/
+// w_scales (two elements per byte, one scale byte per 32 elements).
+hipError_t launch_mx4_quantize(const void* x, int64_t M, int64_t K, void* packed, void* scales,
+                               hipStream_t stream, const LaunchInfo& dev);
+hipError_t launch_mx4_dequantize(const void* packed, const void* scales, int64_t M, int64_t K,
+                                 void* out, hipStream_t stream, const LaunchInfo& dev);
+hipError_t launch_mx4_gemm(const GemmProblem& p, hipStream_t stream, const LaunchInfo& dev);
+
+// Mixture of experts (moe.hip): T tokens of width H, E experts of inner width I.
+struct MoeProblem {
+  const uint16_t* x;        // bf16 [T, H]
+  const float* logits;      // fp32 [T, E]
+  const uint8_t* w13_packed;
+  const uint8_t* w13_scales;
+  const uint8_t* w2_packed;
+  const uint8_t* w2_scales;
+  uint16_t* out;            // bf16 [T, H]
+  int* ids;                 // [T, top_k]
+  float* weights;           // [T, top_k]
+  void* plan;               // moe_plan_bytes(T)
+  uint16_t* h;              // bf16 [T * top_k, I]
+  int64_t T, H, I;
+  int E, top_k;
+  bool renormalize;
+};
+constexpr int64_t kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxTokens = (int64_t)1 << 21;
+int64_t moe_plan_bytes(int64_t T);
+hipError_t launch_moe_router(const void* x, const void* w, int64_t T, int64_t E, int64_t H,
+                             void* logits, hipStream_t stream);
+hipError_t launch_moe(const MoeProblem& p, hipStream_t stream);
+
 hipError_t launch_amax(const void* x, int64_t n, float* out, hipStream_t stream,
                        const LaunchInfo& dev);
 // amax of x, then in place the global scale from it: RN(amax / 2688) clamped into
