@@ -292,6 +292,25 @@ int nvfp4_mxfp4_gemm(const void* a_packed, const void* a_scales, const void* w_p
                      const void* w_scales, int64_t M, int64_t N, int64_t K, void* out_bf16,
                      void* stream);
 
+/* Kernels nvfp4_mxfp4_gemm chooses among (reported by nvfp4_mxfp4_gemm_plan). */
+typedef enum {
+  NVFP4_MXFP4_ROWS = 0,        /* few activation rows: 16 or 32 weight rows per workgroup */
+  NVFP4_MXFP4_SPLIT64 = 1,     /* 64 x 64 output tiles, K split in two within the workgroup */
+  NVFP4_MXFP4_TILE64 = 2,      /* 64 x 64, */
+  NVFP4_MXFP4_TILE64X128 = 3,  /* 64 x 128, */
+  NVFP4_MXFP4_TILE128 = 4,     /* 128 x 128, */
+  NVFP4_MXFP4_TILE128X256 = 5, /* 128 x 256 */
+  NVFP4_MXFP4_TILE256 = 6      /* and 256 x 256 output tiles */
+} nvfp4_mxfp4_kernel;
+
+/*
+ * The kernel nvfp4_mxfp4_gemm launches for an M x N x K product on a device with num_cus
+ * compute units (<= 0: 256, an MI355X). Host only: no device call. Writes an
+ * nvfp4_mxfp4_kernel value to *kernel; NVFP4_ERROR_INVALID_VALUE for a null pointer,
+ * NVFP4_ERROR_INVALID_SHAPE for shapes nvfp4_mxfp4_gemm rejects.
+ */
+int nvfp4_mxfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int num_cus, int* kernel);
+
 /* Workspace bytes nvfp4_mxfp4_linear needs for an [M, K] activation (packed and scales,
  * each rounded up to 256 bytes). Returns 0 for shapes the linear rejects. */
 size_t nvfp4_mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
@@ -300,8 +319,9 @@ size_t nvfp4_mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
  * nvfp4_mxfp4_linear: nvfp4_mxfp4_quantize of x into the workspace, then
  * nvfp4_mxfp4_gemm, both on `stream`. The workspace (16-byte aligned, at least
  * nvfp4_mxfp4_linear_workspace_bytes(M, K) bytes) holds the quantized activations on
- * return: packed [M, K/2] at offset 0, scales [M, K/32] at round_up(M*K/2, 256). Calls that
- * may overlap in time need workspaces of their own.
+ * return: packed [M, K/2] at offset 0, scales [M, K/32] at round_up(M*K/2, 256). At most 16
+ * rows of together at most 24576 elements run as one kernel, with the same bits in the
+ * workspace and the output. Calls that may overlap in time need workspaces of their own.
  */
 int nvfp4_mxfp4_linear(const void* x_bf16, const void* w_packed, const void* w_scales, int64_t M,
                        int64_t N, int64_t K, void* out_bf16, void* workspace,

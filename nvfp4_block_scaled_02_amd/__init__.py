@@ -12,6 +12,7 @@ Python entry points (thin wrappers over the C ABI in include/nvfp4.h):
 * :func:`mxfp8_quantize`, :func:`mxfp8_gemm` -- the MXFP8 (OCP microscaling) path
 * :func:`mxfp4_quantize`, :func:`mxfp4_dequantize`, :func:`mxfp4_gemm`,
   :func:`mxfp4_linear` -- the MXFP4 (OCP microscaling) path
+* :func:`mxfp4_gemm_plan` -- which kernel :func:`mxfp4_gemm` runs a shape on (host only)
 * :func:`moe_router`, :func:`mxfp4_moe` -- a mixture-of-experts layer for a few tokens, its
   experts' weights in MXFP4
 * :func:`fp8r_quantize`, :func:`fp8r_gemm` -- the rowwise FP8 path
@@ -37,6 +38,7 @@ from .ops import (  # noqa: F401
     moe_router,
     mxfp4_dequantize,
     mxfp4_gemm,
+    mxfp4_gemm_plan,
     mxfp4_linear,
     mxfp4_linear_workspace_bytes,
     mxfp4_moe,

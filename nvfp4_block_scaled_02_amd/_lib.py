@@ -50,6 +50,7 @@ SIGNATURES = {
     "nvfp4_mxfp4_quantize": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "nvfp4_mxfp4_dequantize": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "nvfp4_mxfp4_gemm": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "nvfp4_mxfp4_gemm_plan": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int)]),
     "nvfp4_mxfp4_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "nvfp4_mxfp4_linear": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, ctypes.c_size_t, _vp]),
     "nvfp4_moe_router": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp]),

@@ -412,6 +412,14 @@ int nvfp4_mxfp4_gemm(const void* ap, const void* as, const void* wp, const void*
   return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
 }
 
+int nvfp4_mxfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int num_cus, int* kernel) {
+  if (!kernel) return NVFP4_ERROR_INVALID_VALUE;
+  const int s = check_mx4_shape(M, N, K);
+  if (s) return s;
+  *kernel = nvfp4::plan_mx4_gemm(M, N, K, num_cus);
+  return NVFP4_SUCCESS;
+}
+
 size_t nvfp4_mxfp4_linear_workspace_bytes(int64_t M, int64_t K) {
   if (check_mx4_shape(M, 0, K)) return 0;
   return round_up((size_t)(M * (K / 2)), 256) + round_up((size_t)(M * (K / 32)), 256);
@@ -433,11 +441,16 @@ int nvfp4_mxfp4_linear(const void* x, const void* wp, const void* ws, int64_t M,
   nvfp4::LaunchInfo info;
   s = current_device(&info);
   if (s) return s;
-  hipError_t e = nvfp4::launch_mx4_quantize(x, M, K, ap, as, (hipStream_t)stream, info);
-  if (e != hipSuccess) return hip_fail(e);
-  if (N == 0) return NVFP4_SUCCESS;
   nvfp4::GemmProblem p{ap, as, (const uint8_t*)wp, (const uint8_t*)ws, (uint16_t*)out, M, N, K,
                        1.0f, nullptr, nullptr};
+  hipError_t e;
+  if (nvfp4::mx4_linear_fused(M, N, K, info.num_cus)) {
+    e = nvfp4::launch_mx4_linear_fused(p, x, ap, as, (hipStream_t)stream);
+    return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+  }
+  e = nvfp4::launch_mx4_quantize(x, M, K, ap, as, (hipStream_t)stream, info);
+  if (e != hipSuccess) return hip_fail(e);
+  if (N == 0) return NVFP4_SUCCESS;
   e = nvfp4::launch_mx4_gemm(p, (hipStream_t)stream, info);
   return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
 }

@@ -139,6 +139,13 @@ hipError_t launch_mx4_quantize(const void* x, int64_t M, int64_t K, void* packed
 hipError_t launch_mx4_dequantize(const void* packed, const void* scales, int64_t M, int64_t K,
                                  void* out, hipStream_t stream, const LaunchInfo& dev);
 hipError_t launch_mx4_gemm(const GemmProblem& p, hipStream_t stream, const LaunchInfo& dev);
+// The kernel launch_mx4_gemm picks (a value of nvfp4_mxfp4_kernel).
+int plan_mx4_gemm(int64_t M, int64_t N, int64_t K, int64_t cus);
+// The linear in one launch, for a few rows: the product's kernel quantizes the bf16
+// activations x itself (and stores the codes and scales).
+bool mx4_linear_fused(int64_t M, int64_t N, int64_t K, int64_t cus);
+hipError_t launch_mx4_linear_fused(const GemmProblem& p, const void* x, void* packed, void* scales,
+                                   hipStream_t stream);
 
 // Mixture of experts (moe.hip): T tokens of width H, E experts of inner width I.
 struct MoeProblem {

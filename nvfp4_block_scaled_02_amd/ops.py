@@ -287,6 +287,17 @@ def mxfp4_gemm(a_packed: torch.Tensor, a_scales: torch.Tensor, w_packed: torch.T
     return out
 
 
+MXFP4_KERNELS = {0: "rows", 1: "split64", 2: "tile64", 3: "tile64x128", 4: "tile128", 5: "tile128x256", 6: "tile256"}
+
+
+def mxfp4_gemm_plan(M: int, N: int, K: int, num_cus: int = 0) -> str:
+    """Name of the kernel :func:`mxfp4_gemm` launches for an M x N x K product on a device with
+    ``num_cus`` compute units (0: 256, an MI355X). Host only."""
+    kind = ctypes.c_int(-1)
+    check(load_library().nvfp4_mxfp4_gemm_plan(M, N, K, num_cus, ctypes.byref(kind)), "nvfp4_mxfp4_gemm_plan")
+    return MXFP4_KERNELS[kind.value]
+
+
 def mxfp4_linear_workspace_bytes(M: int, K: int) -> int:
     return int(load_library().nvfp4_mxfp4_linear_workspace_bytes(M, K))
 

@@ -119,7 +119,8 @@ def _check_gemm(ops, label, rows=None, cols=None):
 SIZES = [(1, 1, 32), (1, 17, 64), (1, 1000, 96), (1, 4096, 4096), (2, 130, 1440), (5, 33, 288), (16, 257, 512),
          (17, 64, 160), (31, 100, 1024), (32, 512, 2880), (33, 65, 224), (48, 1030, 1056), (64, 64, 8192),
          (65, 129, 736), (100, 300, 320), (127, 255, 256), (128, 128, 128), (129, 1000, 2080), (256, 256, 512),
-         (257, 513, 544), (333, 1001, 1440), (512, 640, 1024), (1000, 96, 768)]
+         (257, 513, 544), (333, 1001, 1440), (512, 640, 1024), (1000, 96, 768),
+         (100, 129, 32), (130, 300, 64), (300, 520, 96), (1100, 1030, 480), (2100, 2050, 352), (70, 2000, 448)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
