@@ -7,6 +7,8 @@
 //   out_t = sum_j g_tj (W2_e h_tj).
 // W13 holds the gate rows Wg and then the up rows Wu of each expert, [E, 2I, H]; W2 is
 // [E, H, I]; both MXFP4 along their last axis.
+#include <type_traits>
+
 #include "gemm_common.hpp"
 
 namespace nvfp4 {
@@ -21,40 +23,79 @@ constexpr int kMoeExperts = (int)kMoeMaxExperts;
 constexpr int kMoeTopK = (int)kMoeMaxTopK;
 constexpr int kMoeSlots = kMoeTokens * kMoeTopK;
 
+// Reductions over a wave in the vector unit (data-parallel primitives: a shift within rows of
+// 16 lanes, then broadcasts across rows); the result is uniform.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRows, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, dpp_or_zero<0x111, 0xF>(v));  // row_shr 1, 2, 4, 8
+  v = max(v, dpp_or_zero<0x112, 0xF>(v));
+  v = max(v, dpp_or_zero<0x114, 0xF>(v));
+  v = max(v, dpp_or_zero<0x118, 0xF>(v));
+  v = max(v, dpp_or_zero<0x142, 0xA>(v));  // row_bcast 15 into rows 1 and 3
+  v = max(v, dpp_or_zero<0x143, 0xC>(v));  // row_bcast 31 into rows 2 and 3
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += u2f(dpp_or_zero<0x111, 0xF>(f2u(v)));
+  v += u2f(dpp_or_zero<0x112, 0xF>(f2u(v)));
+  v += u2f(dpp_or_zero<0x114, 0xF>(f2u(v)));
+  v += u2f(dpp_or_zero<0x118, 0xF>(f2u(v)));
+  v += u2f(dpp_or_zero<0x142, 0xA>(f2u(v)));
+  v += u2f(dpp_or_zero<0x143, 0xC>(f2u(v)));
+  return u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(v), 63));
+}
+
 // ---- the router's product --------------------------------------------------------------
 //
-// logits[t, e] = sum_h x[t, h] w[e, h], each product exact in fp32 (8 x 8 significant bits)
-// and the sum kept in fp64, rounded once to fp32: two experts whose logits differ by more
-// than that rounding are never exchanged by the order of the summation. One wave per
-// expert and group of kTT tokens.
-template <int kTT>
+// logits[t, e] = sum_h x[t, h] w[e, h], summed in fp64 (products of bf16 values are exact
+// there) and rounded once to fp32: two experts whose logits differ by more than that rounding
+// are never exchanged by the order of the summation. A wave takes kE experts and kT tokens,
+// its lanes eight elements of H each in turn; every element is converted once per wave.
+template <int kE, int kT>
 __global__ void __launch_bounds__(256) moe_router_kernel(const u32x4* __restrict__ x,
                                                          const u32x4* __restrict__ w,
                                                          float* __restrict__ logits, int64_t T,
                                                          int64_t E, int64_t H8) {
   const int lane = threadIdx.x & 63;
-  const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t t0 = (int64_t)blockIdx.y * kTT;
-  if (e >= E) return;
-  double acc[kTT] = {};
+  const int64_t e0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kE;
+  const int64_t t0 = (int64_t)blockIdx.y * kT;
+  if (e0 >= E) return;
+  double acc[kE][kT] = {};
   for (int64_t i = lane; i < H8; i += 64) {
-    const u32x4 wv = w[e * H8 + i];
+    u32x4 wv[kE], xv[kT];
 #pragma unroll
-    for (int t = 0; t < kTT; ++t) {
-      const u32x4 xv = x[min(t0 + t, T - 1) * H8 + i];
+    for (int e = 0; e < kE; ++e) wv[e] = w[min(e0 + e, E - 1) * H8 + i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[t] += (double)(u2f(xv[j] << 16) * u2f(wv[j] << 16));
-        acc[t] += (double)(u2f(xv[j] & 0xFFFF0000u) * u2f(wv[j] & 0xFFFF0000u));
+    for (int t = 0; t < kT; ++t) xv[t] = x[min(t0 + t, T - 1) * H8 + i];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      auto element = [&](const u32x4& v) {
+        const uint32_t word = v[j >> 1];
+        return (double)u2f(j & 1 ? word & 0xFFFF0000u : word << 16);
+      };
+      double wd[kE];
+#pragma unroll
+      for (int e = 0; e < kE; ++e) wd[e] = element(wv[e]);
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        const double xd = element(xv[t]);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e][t] = __builtin_fma(xd, wd[e], acc[e][t]);
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < kTT; ++t) {
+  for (int e = 0; e < kE; ++e)
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) acc[t] += __shfl_xor(acc[t], off, 64);
-    if (lane == 0 && t0 + t < T) logits[(t0 + t) * E + e] = (float)acc[t];
-  }
+    for (int t = 0; t < kT; ++t) {
+      double v = acc[e][t];
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+      if (lane == 0 && t0 + t < T && e0 + e < E) logits[(t0 + t) * E + e0 + e] = (float)v;
+    }
 }
 
 // ---- the plan: who goes where ------------------------------------------------------------
@@ -69,103 +110,88 @@ struct MoePlan {
 };
 
 // Order of two logits as an unsigned key: increasing with the value, NaN above +inf, and
-// -inf at 0 (never chosen).
+// -inf at 0 (never chosen). key_logit is its inverse.
 __device__ __forceinline__ uint32_t logit_key(float l) {
   const uint32_t b = f2u(l + 0.0f);  // -0 counts as 0
   if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
   if (b == 0xFF800000u) return 0u;
   return (b >> 31) ? ~b : (b | 0x80000000u);
 }
+__device__ __forceinline__ float key_logit(uint32_t k) { return u2f((k >> 31) ? k ^ 0x80000000u : ~k); }
 
 // The top_k of one token by one wave. Lane l holds experts l, l + 64, ...; each round takes
 // the largest key, the lowest index among equals. A row of fewer than top_k experts that
-// can be chosen ends in slots of id -1 and weight 0.
-__device__ __forceinline__ void moe_topk(const float* __restrict__ row, int E, int top_k,
-                                         bool renormalize, int lane, int* ids, float* weights) {
+// can be chosen ends in slots of id -1 and weight 0. Lane j < top_k returns the j-th choice.
+struct Choice {
+  int id;
+  float weight;
+};
+__device__ __forceinline__ Choice moe_topk(const float* __restrict__ row, int E, int top_k,
+                                           bool renormalize, int lane) {
   constexpr int kPer = kMoeExperts / 64;
-  float l[kPer];
   uint32_t key[kPer];
-  float top = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = e < E ? row[e] : -__builtin_inff();
-    key[i] = logit_key(l[i]);
-    top = l[i] != l[i] ? l[i] : (top != top ? top : __builtin_fmaxf(top, l[i]));
+    key[i] = 0u;
+    if (64 * i < E && lane + 64 * i < E) key[i] = logit_key(row[lane + 64 * i]);
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const float o = __shfl_xor(top, off, 64);
-    top = o != o ? o : (top != top ? top : __builtin_fmaxf(top, o));
-  }
-  float sum = 0.0f;
-  if (!renormalize) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (key[i] != 0u) sum += expf(l[i] - top);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-  }
-  int my_id = -1;        // lane j keeps the j-th choice
-  float my_w = 0.0f;
+  Choice mine = {-1, 0.0f};
+  float top = 0.0f, sum = 0.0f;
   for (int j = 0; j < top_k; ++j) {
-    uint32_t bk = 0u;
-    int be = 0x7FFFFFFF;
-    float bl = 0.0f;
+    uint32_t best = 0u;
+    int at = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (key[i] > bk) {
-        bk = key[i];
-        be = lane + 64 * i;
-        bl = l[i];
+      if (64 * i < E && key[i] > best) {
+        best = key[i];
+        at = i;
       }
+    const uint32_t k = wave_max_u32(best);
+    if (k == 0u) break;  // nothing left to choose
+    const uint32_t e = ~wave_max_u32(best == k ? ~(uint32_t)(lane + 64 * at) : 0u);
+    if (j == 0) {
+      top = key_logit(k);
+      if (!renormalize) {
+        float s = 0.0f;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const uint32_t ok = (uint32_t)__shfl_xor((int)bk, off, 64);
-      const int oe = __shfl_xor(be, off, 64);
-      const float ol = __shfl_xor(bl, off, 64);
-      if (ok > bk || (ok == bk && oe < be)) {
-        bk = ok;
-        be = oe;
-        bl = ol;
+        for (int i = 0; i < kPer; ++i)
+          if (64 * i < E && key[i] != 0u) s += expf(key_logit(key[i]) - top);
+        sum = wave_sum(s);
       }
     }
-    if (bk == 0u) break;  // nothing left to choose (uniform over the wave)
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (lane + 64 * i == be) key[i] = 0u;
-    const float p = expf(bl - top);
+      if (64 * i < E && (uint32_t)(lane + 64 * i) == e) key[i] = 0u;
+    const float p = expf(key_logit(k) - top);
     if (renormalize) sum += p;
-    if (lane == j) {
-      my_id = be;
-      my_w = p;
-    }
+    if (lane == j) mine = Choice{(int)e, p};
   }
-  if (lane < top_k) {
-    ids[lane] = my_id;
-    weights[lane] = my_id < 0 ? 0.0f : my_w / sum;
-  }
+  mine.weight = mine.id < 0 ? 0.0f : mine.weight / sum;
+  return mine;
 }
 
 // One workgroup per chunk.
 __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
   __shared__ int count[kMoeExperts];
   __shared__ int place[kMoeExperts];
+  __shared__ int chosen[kMoeSlots];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t0 = (int64_t)blockIdx.x * kMoeTokens;
   const int nt = (int)min(p.T - t0, (int64_t)kMoeTokens);
   const int n = nt * p.top_k;
   MoePlan* plan = (MoePlan*)p.plan + blockIdx.x;
-  int* ids = p.ids + t0 * p.top_k;
-  float* weights = p.weights + t0 * p.top_k;
   for (int e = threadIdx.x; e < p.E; e += 1024) count[e] = 0;
-  for (int t = wave; t < nt; t += 16)
-    moe_topk(p.logits + (t0 + t) * p.E, p.E, p.top_k, p.renormalize, lane, ids + t * p.top_k,
-             weights + t * p.top_k);
-  __threadfence_block();
+  for (int t = wave; t < nt; t += 16) {
+    const Choice c = moe_topk(p.logits + (t0 + t) * p.E, p.E, p.top_k, p.renormalize, lane);
+    if (lane < p.top_k) {
+      chosen[t * p.top_k + lane] = c.id;
+      p.ids[(t0 + t) * p.top_k + lane] = c.id;
+      p.weights[(t0 + t) * p.top_k + lane] = c.weight;
+    }
+  }
   __syncthreads();
   const int s = threadIdx.x;  // n <= 1024
-  const int e = s < n ? ids[s] : -1;
+  const int e = s < n ? chosen[s] : -1;
   if (e >= 0) atomicAdd(&count[e], 1);
   __syncthreads();
   if (wave == 0) {
@@ -200,30 +226,98 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
 
 // ---- the experts' products --------------------------------------------------------------
 //
-// v_mfma_f32_16x16x32_bf16 with 16 weight rows as its A operand and 16 slots as columns.
-// A lane (q, r) = (lane / 16, lane % 16) takes the 32 elements of block 4 g + q of row r
-// (one 16-byte load, one scale byte) and feeds them to four MFMAs, eight elements each; the
-// activations follow the same order of K. The scaled conversion to bf16 gives a weight's
-// value exactly.
-struct W4Block {
-  u32x4 codes;
-  uint32_t byte;
+// v_mfma_f32_16x16x32_bf16 with 16 weight rows as its A operand and 16 slots as columns; one
+// MFMA multiplies one 32-element block. K goes by units of 512 elements (16 blocks): a lane
+// (q, r) = (lane / 16, lane % 16) loads the 16 bytes of blocks q, 4 + q, 8 + q and 12 + q of
+// row r (64 contiguous bytes of a row per load) and the row's 16 scale bytes. In the MFMA's
+// layout lane (q, r) supplies elements 8q .. 8q + 7 of the block, so the four lanes of a row
+// transpose their 4 x 4 dwords in registers (two swaps of half waves, two of quarter waves),
+// after which register j of a lane is its dword of block 4g + j. An activation load then
+// covers 64 contiguous bytes of each slot's row. The scaled conversion to bf16 gives a
+// weight's value exactly.
+constexpr int kUnit = 16;  // blocks
+
+struct WeightUnit {
+  u32x4 codes[4];
+  u32x4 scales;
 };
-__device__ __forceinline__ W4Block load_block(const uint8_t* codes, const uint8_t* scales,
-                                              int64_t b, int64_t nb) {
-  W4Block w;
-  if (b < nb) {
-    w.codes = __builtin_nontemporal_load((const u32x4*)&codes[16 * b]);
-    w.byte = scales[b];
-  } else {
-    w.codes = u32x4{0u, 0u, 0u, 0u};
-    w.byte = 0u;
+// Unit u of a row of nb blocks starts at block max(min(16 u, nb - 16), 0), so that its 16 scale
+// bytes lie in the row. Blocks before 16 u were the unit before's; a row of fewer than 16
+// blocks is one unit, and has no blocks past nb. Those are cleared (clear_unit).
+__device__ __forceinline__ int unit_start(int u, int nb) { return max(min(kUnit * u, nb - kUnit), 0); }
+__device__ __forceinline__ bool unit_cut(int u, int nb) { return kUnit * u + kUnit > nb; }
+// Whether block b (of the row) is one that unit u multiplies.
+__device__ __forceinline__ bool unit_has(int u, int b, int nb) { return b >= kUnit * u && b < nb; }
+
+// `scales_end`: the end of the scale tensor, at least 16 bytes long. Only in a row of fewer
+// than 16 blocks can the 16 bytes from its start pass it; they are then read before it and
+// shifted down.
+__device__ __forceinline__ void load_unit(WeightUnit& w, const uint8_t* codes, const uint8_t* scales,
+                                          const uint8_t* scales_end, int u, int nb, int q) {
+  const int b0 = unit_start(u, nb);
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    w.codes[g] = __builtin_nontemporal_load((const u32x4*)&codes[16 * (uint32_t)min(b0 + 4 * g + q, nb - 1)]);
+  const int64_t past = nb < kUnit ? max(scales + 16 - scales_end, (int64_t)0) : 0;
+  __builtin_memcpy(&w.scales, scales + b0 - past, 16);
+  if (nb < kUnit) {
+    const uint32_t d = (uint32_t)past;
+    uint32_t s[5] = {w.scales.x, w.scales.y, w.scales.z, w.scales.w, 0u};
+    if (d & 8u) s[0] = s[2], s[1] = s[3], s[2] = s[3] = 0u;
+    if (d & 4u) s[0] = s[1], s[1] = s[2], s[2] = s[3], s[3] = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.scales[i] = __builtin_amdgcn_alignbyte(s[i + 1], s[i], d & 3u);
   }
-  return w;
 }
-__device__ __forceinline__ bf16x8_t decode_part(const W4Block& w, int s) {
-  const float sc = u2f(w.byte << 23);
-  const uint32_t c = w.codes[s];
+// Codes and scale bytes of blocks that are not unit u's: zero.
+__device__ __forceinline__ void clear_unit(WeightUnit& w, int u, int nb, int q) {
+  const int b0 = unit_start(u, nb);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (!unit_has(u, b0 + 4 * g + q, nb)) w.codes[g] = u32x4{0u, 0u, 0u, 0u};
+    uint32_t keep = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep |= unit_has(u, b0 + 4 * g + j, nb) ? 0xFFu << (8 * j) : 0u;
+    w.scales[g] &= keep;
+  }
+}
+
+// A unit's activations of 16 columns: lane (q, r) holds, of each block, elements 8q .. 8q + 7
+// of column r, whose row starts at byte `row` of the window. What a short row has no blocks
+// for is read from beyond it (zeros past the window) and cleared.
+struct ActUnit {
+  u32x4 x[kUnit];
+};
+__device__ __forceinline__ void load_acts(ActUnit& a, __amdgpu_buffer_rsrc_t window, uint32_t row, int u,
+                                          int nb, int q) {
+  const uint32_t at = row + 64u * (uint32_t)unit_start(u, nb) + 16u * (uint32_t)q;
+#pragma unroll
+  for (int b = 0; b < kUnit; ++b)
+    a.x[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(window, (int)(at + 64u * b), 0, 0));
+}
+__device__ __forceinline__ void clear_acts(ActUnit& a, int u, int nb) {
+  const int b0 = unit_start(u, nb);
+#pragma unroll
+  for (int b = 0; b < kUnit; ++b)
+    if (!unit_has(u, b0 + b, nb)) a.x[b] = u32x4{0u, 0u, 0u, 0u};
+}
+
+// Dwords of the lanes (q = 0..3, r) transposed: out[j] of lane q = in[q] of lane j.
+__device__ __forceinline__ void transpose4(const u32x4 in, uint32_t* out) {
+  const uint32_t a = in.x, b = in.y, c = in.z, d = in.w;
+  const auto ac = __builtin_amdgcn_permlane32_swap(a, c, false, false);
+  const auto bd = __builtin_amdgcn_permlane32_swap(b, d, false, false);
+  const auto lo = __builtin_amdgcn_permlane16_swap(ac[0], bd[0], false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(ac[1], bd[1], false, false);
+  out[0] = lo[0];
+  out[1] = lo[1];
+  out[2] = hi[0];
+  out[3] = hi[1];
+}
+
+// Eight codes under the scale of byte j of `bytes`, as bf16.
+__device__ __forceinline__ bf16x8_t decode8_bf16(uint32_t c, uint32_t bytes, int j) {
+  const float sc = u2f(((bytes >> (8 * j)) & 0xFFu) << 23);
   const u32x4 o = {
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 0)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 1)),
@@ -231,111 +325,287 @@ __device__ __forceinline__ bf16x8_t decode_part(const W4Block& w, int s) {
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 3))};
   return __builtin_bit_cast(bf16x8_t, o);
 }
-__device__ __forceinline__ u32x4 load_x(const uint16_t* row, int64_t b, int64_t nb, int s) {
-  return b < nb ? *(const u32x4*)&row[32 * b + 8 * s] : u32x4{0u, 0u, 0u, 0u};
-}
 
-// h[slot, i] = silu(gate) * up for 16 gate rows and their 16 up rows of one expert and up
-// to 64 slots: four waves split K and meet in LDS.
-__global__ void __launch_bounds__(256) moe_gate_up_kernel(MoeProblem p) {
-  constexpr int NW = 4, kTiles = kMoeTokens / 16;
-  __shared__ floatx4 part[NW][2][64];
-  const MoePlan* plan = (const MoePlan*)p.plan + blockIdx.z;
-  const int a = blockIdx.y;
-  if (a >= plan->active) return;
-  const int64_t e = plan->expert[a];
-  const int s0 = plan->first[a], ns = plan->first[a + 1] - s0;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int q = lane >> 4, r = lane & 15;
-  const int64_t i0 = (int64_t)blockIdx.x * 16;
-  const int64_t nb = p.H >> 5;
-  const int64_t t0 = (int64_t)blockIdx.z * kMoeTokens;
-  const int64_t grow = e * 2 * p.I + i0 + r, urow = grow + p.I;
-  const uint8_t* gc = p.w13_packed + grow * (p.H >> 1);
-  const uint8_t* uc = p.w13_packed + urow * (p.H >> 1);
-  const uint8_t* gs = p.w13_scales + grow * nb;
-  const uint8_t* us = p.w13_scales + urow * nb;
-  for (int c0 = 0; c0 < ns; c0 += 16) {
-    const int slot = plan->slot[s0 + min(c0 + r, ns - 1)];
-    const uint16_t* xr = p.x + (t0 + slot / p.top_k) * p.H;
-    floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f}, u = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t b0 = 4 * wave; b0 < nb; b0 += 4 * NW) {
-      const W4Block gw = load_block(gc, gs, b0 + q, nb), uw = load_block(uc, us, b0 + q, nb);
+// acc[f][t] += the unit of weights w[f] times tile t's activations: fetch(b, t) gives the
+// unit's block b, eight of its bf16 values of this lane's column.
+template <int kF, int kT, typename Fetch>
+__device__ __forceinline__ void multiply_unit(floatx4 (&acc)[kF][kT], const WeightUnit (&w)[kF],
+                                              const Fetch& fetch) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bf16x8_t xv = __builtin_bit_cast(bf16x8_t, load_x(xr, b0 + q, nb, s));
-        g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode_part(gw, s), xv, g, 0, 0, 0);
-        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode_part(uw, s), xv, u, 0, 0, 0);
+  for (int g = 0; g < 4; ++g) {
+    u32x4 x[4][kT];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < kT; ++t) x[j][t] = fetch(4 * g + j, t);
+    uint32_t c[kF][4];
+#pragma unroll
+    for (int f = 0; f < kF; ++f) transpose4(w[f].codes[g], c[f]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int f = 0; f < kF; ++f) {
+        const bf16x8_t wv = decode8_bf16(c[f][j], w[f].scales[g], j);
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+          acc[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8_t, x[j][t]),
+                                                              acc[f][t], 0, 0, 0);
       }
     }
+    // (without a fence the decodes of all groups are moved ahead of the MFMAs, into registers
+    // that are not there)
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// silu(g) * u of four rows, as bf16: h is rounded to the type of the activations that the next
+// product takes.
+__device__ __forceinline__ u32x2 gated(const floatx4 g, const floatx4 u) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
+  return bf16x4_rne(v[0], v[1], v[2], v[3]);
+}
+
+constexpr int kTiles = kMoeTokens / 16;
+constexpr int kGateWaves = 4;
+
+// One expert's part of a launch.
+struct ExpertSlots {
+  int64_t expert;
+  const int* slots;
+  int n;
+};
+__device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s) {
+  const MoePlan* plan = (const MoePlan*)p.plan + blockIdx.z;
+  const int a = blockIdx.y;
+  s.expert = plan->expert[a];  // (of no meaning past the active ones, but in the buffer)
+  s.slots = plan->slot + plan->first[a];
+  s.n = plan->first[a + 1] - plan->first[a];
+  return a < plan->active;
+}
+
+// This lane's gate and up rows.
+struct GateRows {
+  const uint8_t *gate, *up, *gate_scales, *up_scales, *scales_end;
+  __device__ __forceinline__ GateRows(const MoeProblem& p, int64_t expert, int64_t i) {
+    const int64_t grow = expert * 2 * p.I + i, urow = grow + p.I;
+    gate = p.w13_packed + grow * (p.H >> 1);
+    up = p.w13_packed + urow * (p.H >> 1);
+    gate_scales = p.w13_scales + grow * (p.H >> 5);
+    up_scales = p.w13_scales + urow * (p.H >> 5);
+    scales_end = p.w13_scales + (int64_t)p.E * 2 * p.I * (p.H >> 5);
+  }
+  __device__ __forceinline__ void load(WeightUnit (&w)[2], int u, int nb, int q) const {
+    load_unit(w[0], gate, gate_scales, scales_end, u, nb, q);
+    load_unit(w[1], up, up_scales, scales_end, u, nb, q);
+  }
+};
+
+// h[slot, i] = silu(gate) * up, few experts reached: 16 gate rows and their up rows per
+// workgroup, whose waves take units of K in turn, a unit's weights and activations in flight at
+// once, and meet in LDS.
+__global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(MoeProblem p) {
+  constexpr int NW = kGateWaves;
+  __shared__ floatx4 part[NW][2][64];
+  ExpertSlots s;
+  if (!expert_slots(p, s)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  const int64_t i0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.z * kMoeTokens;
+  const int nb = (int)(p.H >> 5), nu = (nb + kUnit - 1) / kUnit;
+  const GateRows rows(p, s.expert, i0 + r);
+  const int64_t tokens = min(p.T - t0, (int64_t)kMoeTokens);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + t0 * p.H, (uint32_t)(tokens * p.H * 2));
+  uint16_t* h = p.h + t0 * p.top_k * p.I + i0;
+  for (int c0 = 0; c0 < s.n; c0 += 16) {
+    const int slot = s.slots[min(c0 + r, s.n - 1)];
+    const uint32_t row = (uint32_t)(slot / p.top_k) * (uint32_t)(p.H * 2);
+    WeightUnit w[2];
+    ActUnit x;
+    floatx4 acc[2][1];
+    acc[0][0] = acc[1][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int u = wave; u < nu; u += NW) {
+      rows.load(w, u, nb, q);
+      load_acts(x, rx, row, u, nb, q);
+      __builtin_amdgcn_sched_barrier(0);
+      if (unit_cut(u, nb)) {
+        clear_unit(w[0], u, nb, q);
+        clear_unit(w[1], u, nb, q);
+        clear_acts(x, u, nb);
+      }
+      multiply_unit<2, 1>(acc, w, [&](int b, int) { return x.x[b]; });
+    }
     __syncthreads();
-    part[wave][0][lane] = g;
-    part[wave][1][lane] = u;
+    part[wave][0][lane] = acc[0][0];
+    part[wave][1][lane] = acc[1][0];
     __syncthreads();
-    if (wave == 0 && c0 + r < ns) {
+    if (wave == 0 && c0 + r < s.n) {
+      floatx4 g = acc[0][0], v = acc[1][0];
 #pragma unroll
       for (int w = 1; w < NW; ++w) {
         g += part[w][0][lane];
-        u += part[w][1][lane];
+        v += part[w][1][lane];
       }
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
-      // h is rounded to bf16, the type of the activations that the next product takes
-      *(u32x2*)&p.h[(t0 * p.top_k + slot) * p.I + i0 + 4 * q] = bf16x4_rne(v[0], v[1], v[2], v[3]);
+      *(u32x2*)&h[(uint32_t)slot * (uint32_t)p.I + 4 * q] = gated(g, v);
     }
   }
-  (void)kTiles;
+}
+
+// The same for many experts: 64 gate rows and their up rows per workgroup, 16 + 16 per wave,
+// each wave over the whole of K, with the activations of a unit staged in LDS for all of them
+// (direct loads of one slot's 1 KiB per instruction). Chunk c (16 bytes) of row s sits at slot
+// c ^ (s % 16), so that the 16 columns of a fragment read are in distinct banks.
+// One barrier per unit: behind it the unit is readable, and the buffer of the unit before
+// takes the next. kT tiles of 16 slots; above 32 slots one buffer, filled between two barriers.
+template <int kT>
+__device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertSlots& s, const GateRows& rows,
+                                              bool mine, int64_t t0, int64_t i0, int wave, int lane,
+                                              uint8_t* lds) {
+  constexpr int kBufs = kT <= 2 ? 2 : 1, kBytes = kT * 16 * 1024;
+  const int q = lane >> 4, r = lane & 15;
+  const int nb = (int)(p.H >> 5), nu = (nb + kUnit - 1) / kUnit;
+  const int64_t tokens = min(p.T - t0, (int64_t)kMoeTokens);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + t0 * p.H, (uint32_t)(tokens * p.H * 2));
+  int slot[kT];      // of this lane's columns
+  uint32_t row0[kT];  // and where their activations start
+#pragma unroll
+  for (int t = 0; t < kT; ++t) {
+    slot[t] = s.slots[min(16 * t + r, s.n - 1)];
+    row0[t] = (uint32_t)(slot[t] / p.top_k) * (uint32_t)(p.H * 2);
+  }
+  auto stage = [&](int u, int buf) {
+    const uint32_t at = (uint32_t)unit_start(u, nb) * 64u;
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int k = 0; k < 16 / kGateWaves; ++k) {
+        const int row = kGateWaves * k + wave;  // of tile t
+        if (16 * t + row >= s.n) continue;
+        const int chunk = lane ^ row;
+        // blocks that are not the unit's lie past the window: zeros
+        const uint32_t past = unit_has(u, unit_start(u, nb) + (chunk >> 2), nb) ? 0u : 0x80000000u;
+        const uint32_t start = (uint32_t)__builtin_amdgcn_readlane((int)row0[t], row);
+        buffer_load_lds16(rx, lds + buf * kBytes + (16 * t + row) * 1024, (start + 16u * (uint32_t)chunk) | past, at);
+      }
+  };
+  WeightUnit cur[2], nxt[2];
+  if (mine) rows.load(cur, 0, nb, q);
+  stage(0, 0);
+  floatx4 acc[2][kT];
+#pragma unroll
+  for (int t = 0; t < kT; ++t) acc[0][t] = acc[1][t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int u = 0; u < nu; ++u) {
+    const int buf = kBufs == 2 ? u & 1 : 0;
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    if (u + 1 < nu) {
+      if (mine) rows.load(nxt, u + 1, nb, q);
+      if (kBufs == 2) stage(u + 1, buf ^ 1);
+    }
+    if (mine) {
+      if (unit_cut(u, nb)) {
+        clear_unit(cur[0], u, nb, q);
+        clear_unit(cur[1], u, nb, q);
+      }
+      multiply_unit<2, kT>(acc, cur, [&](int b, int t) {
+        return *(const u32x4*)&lds[buf * kBytes + (16 * t + r) * 1024 + 16 * ((4 * b + q) ^ r)];
+      });
+    }
+    if (kBufs == 1 && u + 1 < nu) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      stage(u + 1, 0);
+    }
+    cur[0] = nxt[0];
+    cur[1] = nxt[1];
+  }
+  if (!mine) return;
+  uint16_t* h = p.h + t0 * p.top_k * p.I + i0;
+#pragma unroll
+  for (int t = 0; t < kT; ++t)
+    if (16 * t + r < s.n)
+      *(u32x2*)&h[(uint32_t)slot[t] * (uint32_t)p.I + 4 * q] = gated(acc[0][t], acc[1][t]);
+}
+
+__global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProblem p) {
+  __shared__ __align__(16) uint8_t lds[kTiles * 16 * 1024];
+  ExpertSlots s;
+  if (!expert_slots(p, s)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t i0 = (int64_t)blockIdx.x * (16 * kGateWaves) + 16 * wave, t0 = (int64_t)blockIdx.z * kMoeTokens;
+  const bool mine = i0 < p.I;  // I % 32 == 0: a wave's 16 rows are all there or none
+  const GateRows rows(p, s.expert, mine ? i0 + (lane & 15) : 0);
+  if (s.n <= 16) gate_up_tiles<1>(p, s, rows, mine, t0, i0, wave, lane, lds);
+  else if (s.n <= 32) gate_up_tiles<2>(p, s, rows, mine, t0, i0, wave, lane, lds);
+  else gate_up_tiles<4>(p, s, rows, mine, t0, i0, wave, lane, lds);
 }
 
 // out[t, o] for 16 rows of W2 and one chunk of tokens: the workgroup's waves take (expert,
-// K) parts in turn and each adds its weighted results to its own fp32 sums by token; the
-// waves' sums are added in a fixed order.
-__global__ void __launch_bounds__(512) moe_down_kernel(MoeProblem p) {
+// unit of K) pairs in turn, each with its next pair's weights in flight, and add the weighted results to their own fp32 sums by token in LDS; the waves' sums
+// are added in a fixed order.
+__global__ void __launch_bounds__(512, 2) moe_down_kernel(MoeProblem p) {
   constexpr int NW = 8;
-  __shared__ float sums[NW][kMoeTokens][16];
+  __shared__ floatx4 sums[NW][kMoeTokens][4];
+  __shared__ int s_expert[kMoeExperts];
+  __shared__ int s_first[kMoeExperts + 1];
+  __shared__ int s_slot[kMoeSlots];
   const MoePlan* plan = (const MoePlan*)p.plan + blockIdx.z;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15;
   const int64_t o0 = (int64_t)blockIdx.x * 16;
-  const int64_t nb = p.I >> 5;
+  const int nb = (int)(p.I >> 5), nu = (nb + kUnit - 1) / kUnit;
   const int64_t t0 = (int64_t)blockIdx.z * kMoeTokens;
   const int nt = (int)min(p.T - t0, (int64_t)kMoeTokens);
-  for (int i = threadIdx.x; i < NW * kMoeTokens * 16; i += 64 * NW) (&sums[0][0][0])[i] = 0.0f;
-  __syncthreads();
+  const int n = nt * p.top_k, most = min(n, p.E);
   const int active = plan->active;
-  for (int a = wave; a < active; a += NW) {
-    const int64_t e = plan->expert[a];
-    const int s0 = plan->first[a], ns = plan->first[a + 1] - s0;
-    const int64_t row = e * p.H + o0 + r;
-    const uint8_t* wc = p.w2_packed + row * (p.I >> 1);
-    const uint8_t* ws = p.w2_scales + row * nb;
+  // the plan's lists, as long as they can be (past the active experts: of no meaning)
+  for (int i = threadIdx.x; i < most; i += 64 * NW) s_expert[i] = plan->expert[i];
+  for (int i = threadIdx.x; i <= most; i += 64 * NW) s_first[i] = plan->first[i];
+  for (int i = threadIdx.x; i < n; i += 64 * NW) s_slot[i] = plan->slot[i];
+  for (int i = threadIdx.x; i < NW * nt * 4; i += 64 * NW)
+    sums[i / (nt * 4)][i % (nt * 4) >> 2][i & 3] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  __syncthreads();
+  const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.h + t0 * p.top_k * p.I, (uint32_t)(n * p.I * 2));
+  const float* weights = p.weights + t0 * p.top_k;
+  const uint8_t* scales_end = p.w2_scales + (int64_t)p.E * p.H * nb;
+  const int pairs = active * nu;
+  WeightUnit cur[1], nxt[1];
+  auto load = [&](WeightUnit& w, int at) {
+    const int64_t row = (int64_t)s_expert[at / nu] * p.H + o0 + r;
+    load_unit(w, p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb, scales_end, at % nu, nb, q);
+  };
+  if (wave < pairs) load(cur[0], wave);
+  for (int at = wave; at < pairs; at += NW) {
+    const int a = at / nu, u = at % nu, s0 = s_first[a], ns = s_first[a + 1] - s0;
+    ActUnit x;
+    load_acts(x, rh, (uint32_t)s_slot[s0 + min(r, ns - 1)] * (uint32_t)(p.I * 2), u, nb, q);
+    if (at + NW < pairs) load(nxt[0], at + NW);
+    __builtin_amdgcn_sched_barrier(0);
+    if (unit_cut(u, nb)) clear_unit(cur[0], u, nb, q);
     for (int c0 = 0; c0 < ns; c0 += 16) {
-      const int slot = plan->slot[s0 + min(c0 + r, ns - 1)];
-      const uint16_t* hr = p.h + (t0 * p.top_k + slot) * p.I;
-      floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int64_t b0 = 0; b0 < nb; b0 += 4) {
-        const W4Block w = load_block(wc, ws, b0 + q, nb);
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              decode_part(w, s), __builtin_bit_cast(bf16x8_t, load_x(hr, b0 + q, nb, s)), acc, 0, 0, 0);
-      }
+      if (c0 > 0) load_acts(x, rh, (uint32_t)s_slot[s0 + min(c0 + r, ns - 1)] * (uint32_t)(p.I * 2), u, nb, q);
+      if (unit_cut(u, nb)) clear_acts(x, u, nb);
+      floatx4 acc[1][1];
+      acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      multiply_unit<1, 1>(acc, cur, [&](int b, int) { return x.x[b]; });
       if (c0 + r < ns) {
-        const float g = p.weights[t0 * p.top_k + slot];
-        float* to = &sums[wave][slot / p.top_k][4 * q];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] += g * acc[i];
+        const int slot = s_slot[s0 + c0 + r];
+        sums[wave][slot / p.top_k][q] += weights[slot] * acc[0][0];
       }
     }
+    cur[0] = nxt[0];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < nt * 16; i += 64 * NW) {
-    const int t = i >> 4, o = i & 15;
-    float v = 0.0f;
+  for (int i = threadIdx.x; i < nt * 4; i += 64 * NW) {
+    const int t = i >> 2, o = i & 3;
+    floatx4 v = sums[0][t][o];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += sums[w][t][o];
-    p.out[(t0 + t) * p.H + o0 + o] = (uint16_t)bf16x2_rne(v, 0.0f);
+    for (int w = 1; w < NW; ++w) v += sums[w][t][o];
+    *(u32x2*)&p.out[(t0 + t) * p.H + o0 + 4 * o] = bf16x4_rne(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -347,10 +617,14 @@ int64_t moe_plan_bytes(int64_t T) {
 
 hipError_t launch_moe_router(const void* x, const void* w, int64_t T, int64_t E, int64_t H,
                              void* logits, hipStream_t stream) {
-  constexpr int kTT = 4;
-  const dim3 grid((unsigned)((E + 3) / 4), (unsigned)((T + kTT - 1) / kTT));
-  hipLaunchKernelGGL((moe_router_kernel<kTT>), grid, dim3(256), 0, stream, (const u32x4*)x,
-                     (const u32x4*)w, (float*)logits, T, E, H / 8);
+  // one or two tokens: an expert per wave, the most waves; more: blocks of 2 experts x 4 tokens
+  if (T <= 2) {
+    hipLaunchKernelGGL((moe_router_kernel<1, 1>), dim3((unsigned)((E + 3) / 4), (unsigned)T), dim3(256), 0,
+                       stream, (const u32x4*)x, (const u32x4*)w, (float*)logits, T, E, H / 8);
+  } else {
+    hipLaunchKernelGGL((moe_router_kernel<2, 4>), dim3((unsigned)((E + 7) / 8), (unsigned)((T + 3) / 4)),
+                       dim3(256), 0, stream, (const u32x4*)x, (const u32x4*)w, (float*)logits, T, E, H / 8);
+  }
   return hipGetLastError();
 }
 
@@ -361,8 +635,12 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   hipLaunchKernelGGL(moe_plan_kernel, dim3(chunks), dim3(1024), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_gate_up_kernel, dim3((unsigned)(p.I / 16), most, chunks), dim3(256), 0,
-                     stream, p);
+  const unsigned wide = (unsigned)((p.I + 63) / 64);
+  if ((int64_t)wide * most * chunks >= 512)
+    hipLaunchKernelGGL(moe_gate_up_kernel, dim3(wide, most, chunks), dim3(64 * kGateWaves), 0, stream, p);
+  else
+    hipLaunchKernelGGL(moe_gate_up_split_kernel, dim3((unsigned)(p.I / 16), most, chunks),
+                       dim3(64 * kGateWaves), 0, stream, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16), 1, chunks), dim3(512), 0, stream, p);
