@@ -226,20 +226,22 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
 
 // ---- the experts' products --------------------------------------------------------------
 //
-// v_mfma_f32_16x16x32_bf16 with 16 weight rows as its A operand and 16 slots as columns; one
-// MFMA multiplies one 32-element block. K goes by units of 512 elements (16 blocks): a lane
-// (q, r) = (lane / 16, lane % 16) loads the 16 bytes of blocks q, 4 + q, 8 + q and 12 + q of
-// row r (64 contiguous bytes of a row per load) and the row's 16 scale bytes. In the MFMA's
-// layout lane (q, r) supplies elements 8q .. 8q + 7 of the block, so the four lanes of a row
-// transpose their 4 x 4 dwords in registers (two swaps of half waves, two of quarter waves),
-// after which register j of a lane is its dword of block 4g + j. An activation load then
-// covers 64 contiguous bytes of each slot's row. The scaled conversion to bf16 gives a
-// weight's value exactly.
+// v_mfma_f32_16x16x32_bf16 with 16 weight rows as its A operand and 16 slots as columns. K
+// goes by units of 512 elements (16 blocks). In the matrix instruction a lane (q, r) =
+// (lane / 16, lane % 16) stands for row r, so that neighbouring lanes are different rows; a
+// load made in that order takes a cache access for every lane (measured: it bounded these
+// kernels, not memory). So the weights are loaded in the order of memory, four lanes to the 64
+// bytes of blocks 4g .. 4g + 3 of a row, and handed over to lane (q, r), which gets block 4g + q
+// of row r, by lane permutes through the LDS crossbar. Its four dwords go into four MFMAs,
+// eight elements each; the activations follow the same order of K. The scaled conversion to
+// bf16 gives a weight's value exactly.
 constexpr int kUnit = 16;  // blocks
 
+// As loaded by lane l: row l / 4, of every four blocks the block l % 4, and of the 16 scale bytes
+// the dword l % 4.
 struct WeightUnit {
   u32x4 codes[4];
-  u32x4 scales;
+  uint32_t scales;
 };
 // Unit u of a row of nb blocks starts at block max(min(16 u, nb - 16), 0), so that its 16 scale
 // bytes lie in the row. Blocks before 16 u were the unit before's; a row of fewer than 16
@@ -249,75 +251,62 @@ __device__ __forceinline__ bool unit_cut(int u, int nb) { return kUnit * u + kUn
 // Whether block b (of the row) is one that unit u multiplies.
 __device__ __forceinline__ bool unit_has(int u, int b, int nb) { return b >= kUnit * u && b < nb; }
 
-// `scales_end`: the end of the scale tensor, at least 16 bytes long. Only in a row of fewer
-// than 16 blocks can the 16 bytes from its start pass it; they are then read before it and
-// shifted down.
-__device__ __forceinline__ void load_unit(WeightUnit& w, const uint8_t* codes, const uint8_t* scales,
-                                          const uint8_t* scales_end, int u, int nb, int q) {
-  const int b0 = unit_start(u, nb);
+__device__ __forceinline__ void load_unit(WeightUnit& w, const uint8_t* codes, const uint8_t* scales, int u,
+                                          int nb, int lane) {
+  const int b0 = unit_start(u, nb), part = lane & 3;
 #pragma unroll
   for (int g = 0; g < 4; ++g)
-    w.codes[g] = __builtin_nontemporal_load((const u32x4*)&codes[16 * (uint32_t)min(b0 + 4 * g + q, nb - 1)]);
-  const int64_t past = nb < kUnit ? max(scales + 16 - scales_end, (int64_t)0) : 0;
-  __builtin_memcpy(&w.scales, scales + b0 - past, 16);
-  if (nb < kUnit) {
-    const uint32_t d = (uint32_t)past;
-    uint32_t s[5] = {w.scales.x, w.scales.y, w.scales.z, w.scales.w, 0u};
-    if (d & 8u) s[0] = s[2], s[1] = s[3], s[2] = s[3] = 0u;
-    if (d & 4u) s[0] = s[1], s[1] = s[2], s[2] = s[3], s[3] = 0u;
+    w.codes[g] = *(const u32x4*)&codes[16 * (uint32_t)min(b0 + 4 * g + part, nb - 1)];
+  if (nb >= kUnit) {
+    __builtin_memcpy(&w.scales, scales + b0 + 4 * part, 4);  // at any alignment
+  } else {
+    uint32_t s = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w.scales[i] = __builtin_amdgcn_alignbyte(s[i + 1], s[i], d & 3u);
+    for (int i = 0; i < 4; ++i) s |= (uint32_t)scales[min(4 * part + i, nb - 1)] << (8 * i);
+    w.scales = s;
   }
 }
 // Codes and scale bytes of blocks that are not unit u's: zero.
-__device__ __forceinline__ void clear_unit(WeightUnit& w, int u, int nb, int q) {
-  const int b0 = unit_start(u, nb);
+__device__ __forceinline__ void clear_unit(WeightUnit& w, int u, int nb, int lane) {
+  const int b0 = unit_start(u, nb), part = lane & 3;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    if (!unit_has(u, b0 + 4 * g + q, nb)) w.codes[g] = u32x4{0u, 0u, 0u, 0u};
-    uint32_t keep = 0u;
+  for (int g = 0; g < 4; ++g)
+    if (!unit_has(u, b0 + 4 * g + part, nb)) w.codes[g] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) keep |= unit_has(u, b0 + 4 * g + j, nb) ? 0xFFu << (8 * j) : 0u;
-    w.scales[g] &= keep;
-  }
+  for (int i = 0; i < 4; ++i)
+    if (!unit_has(u, b0 + 4 * part + i, nb)) w.scales &= ~(0xFFu << (8 * i));
 }
 
-// A unit's activations of 16 columns: lane (q, r) holds, of each block, elements 8q .. 8q + 7
-// of column r, whose row starts at byte `row` of the window. What a short row has no blocks
-// for is read from beyond it (zeros past the window) and cleared.
+// A unit's activations of 16 columns: lane (q, r) holds, of column r, elements 8j .. 8j + 7 of
+// block 4g + q in x[4 g + j]. The column's row starts at byte `row` of the window. What a short
+// row has no blocks for is read from beyond it (zeros past the window) and cleared. Lanes of
+// columns that are not there (`have` false) load nothing: a column's results depend on its own
+// activations alone.
 struct ActUnit {
   u32x4 x[kUnit];
 };
-__device__ __forceinline__ void load_acts(ActUnit& a, __amdgpu_buffer_rsrc_t window, uint32_t row, int u,
-                                          int nb, int q) {
-  const uint32_t at = row + 64u * (uint32_t)unit_start(u, nb) + 16u * (uint32_t)q;
+__device__ __forceinline__ void load_acts(ActUnit& a, __amdgpu_buffer_rsrc_t window, bool have, uint32_t row,
+                                          int u, int nb, int q) {
+  if (!have) return;
+  const uint32_t at = row + 64u * (uint32_t)(unit_start(u, nb) + q);
 #pragma unroll
-  for (int b = 0; b < kUnit; ++b)
-    a.x[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(window, (int)(at + 64u * b), 0, 0));
+  for (int i = 0; i < kUnit; ++i)
+    a.x[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+        window, (int)(at + 256u * (uint32_t)(i >> 2) + 16u * (uint32_t)(i & 3)), 0, 0));
 }
-__device__ __forceinline__ void clear_acts(ActUnit& a, int u, int nb) {
+__device__ __forceinline__ void clear_acts(ActUnit& a, int u, int nb, int q) {
   const int b0 = unit_start(u, nb);
 #pragma unroll
-  for (int b = 0; b < kUnit; ++b)
-    if (!unit_has(u, b0 + b, nb)) a.x[b] = u32x4{0u, 0u, 0u, 0u};
+  for (int i = 0; i < kUnit; ++i)
+    if (!unit_has(u, b0 + 4 * (i >> 2) + q, nb)) a.x[i] = u32x4{0u, 0u, 0u, 0u};
 }
 
-// Dwords of the lanes (q = 0..3, r) transposed: out[j] of lane q = in[q] of lane j.
-__device__ __forceinline__ void transpose4(const u32x4 in, uint32_t* out) {
-  const uint32_t a = in.x, b = in.y, c = in.z, d = in.w;
-  const auto ac = __builtin_amdgcn_permlane32_swap(a, c, false, false);
-  const auto bd = __builtin_amdgcn_permlane32_swap(b, d, false, false);
-  const auto lo = __builtin_amdgcn_permlane16_swap(ac[0], bd[0], false, false);
-  const auto hi = __builtin_amdgcn_permlane16_swap(ac[1], bd[1], false, false);
-  out[0] = lo[0];
-  out[1] = lo[1];
-  out[2] = hi[0];
-  out[3] = hi[1];
+__device__ __forceinline__ uint32_t from_lane(int lane, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_ds_bpermute(4 * lane, (int)v);
 }
 
-// Eight codes under the scale of byte j of `bytes`, as bf16.
-__device__ __forceinline__ bf16x8_t decode8_bf16(uint32_t c, uint32_t bytes, int j) {
-  const float sc = u2f(((bytes >> (8 * j)) & 0xFFu) << 23);
+// Eight codes under a scale, as bf16.
+__device__ __forceinline__ bf16x8_t decode8_bf16(uint32_t c, float sc) {
   const u32x4 o = {
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 0)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 1)),
@@ -326,11 +315,12 @@ __device__ __forceinline__ bf16x8_t decode8_bf16(uint32_t c, uint32_t bytes, int
   return __builtin_bit_cast(bf16x8_t, o);
 }
 
-// acc[f][t] += the unit of weights w[f] times tile t's activations: fetch(b, t) gives the
-// unit's block b, eight of its bf16 values of this lane's column.
+// acc[f][t] += the unit of weights w[f] times tile t's activations: fetch(i, t) gives entry i of
+// an ActUnit of this lane's column.
 template <int kF, int kT, typename Fetch>
-__device__ __forceinline__ void multiply_unit(floatx4 (&acc)[kF][kT], const WeightUnit (&w)[kF],
+__device__ __forceinline__ void multiply_unit(floatx4 (&acc)[kF][kT], const WeightUnit (&w)[kF], int lane,
                                               const Fetch& fetch) {
+  const int q = lane >> 4, r = lane & 15;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     u32x4 x[4][kT];
@@ -339,13 +329,22 @@ __device__ __forceinline__ void multiply_unit(floatx4 (&acc)[kF][kT], const Weig
 #pragma unroll
       for (int t = 0; t < kT; ++t) x[j][t] = fetch(4 * g + j, t);
     uint32_t c[kF][4];
+    float sc[kF];
 #pragma unroll
-    for (int f = 0; f < kF; ++f) transpose4(w[f].codes[g], c[f]);
+    for (int f = 0; f < kF; ++f) {
+      const uint32_t bytes = from_lane(4 * r + g, w[f].scales);
+      sc[f] = u2f(((bytes >> (8 * q)) & 0xFFu) << 23);
+      const uint32_t c0 = w[f].codes[g].x, c1 = w[f].codes[g].y, c2 = w[f].codes[g].z, c3 = w[f].codes[g].w;
+      c[f][0] = from_lane(4 * r + q, c0);
+      c[f][1] = from_lane(4 * r + q, c1);
+      c[f][2] = from_lane(4 * r + q, c2);
+      c[f][3] = from_lane(4 * r + q, c3);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
       for (int f = 0; f < kF; ++f) {
-        const bf16x8_t wv = decode8_bf16(c[f][j], w[f].scales[g], j);
+        const bf16x8_t wv = decode8_bf16(c[f][j], sc[f]);
 #pragma unroll
         for (int t = 0; t < kT; ++t)
           acc[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8_t, x[j][t]),
@@ -385,20 +384,19 @@ __device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s
   return a < plan->active;
 }
 
-// This lane's gate and up rows.
+// The gate and up rows that this lane loads of (row lane / 4 of 16).
 struct GateRows {
-  const uint8_t *gate, *up, *gate_scales, *up_scales, *scales_end;
+  const uint8_t *gate, *up, *gate_scales, *up_scales;
   __device__ __forceinline__ GateRows(const MoeProblem& p, int64_t expert, int64_t i) {
     const int64_t grow = expert * 2 * p.I + i, urow = grow + p.I;
     gate = p.w13_packed + grow * (p.H >> 1);
     up = p.w13_packed + urow * (p.H >> 1);
     gate_scales = p.w13_scales + grow * (p.H >> 5);
     up_scales = p.w13_scales + urow * (p.H >> 5);
-    scales_end = p.w13_scales + (int64_t)p.E * 2 * p.I * (p.H >> 5);
   }
-  __device__ __forceinline__ void load(WeightUnit (&w)[2], int u, int nb, int q) const {
-    load_unit(w[0], gate, gate_scales, scales_end, u, nb, q);
-    load_unit(w[1], up, up_scales, scales_end, u, nb, q);
+  __device__ __forceinline__ void load(WeightUnit (&w)[2], int u, int nb, int lane) const {
+    load_unit(w[0], gate, gate_scales, u, nb, lane);
+    load_unit(w[1], up, up_scales, u, nb, lane);
   }
 };
 
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(M
   const int q = lane >> 4, r = lane & 15;
   const int64_t i0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const int nb = (int)(p.H >> 5), nu = (nb + kUnit - 1) / kUnit;
-  const GateRows rows(p, s.expert, i0 + r);
+  const GateRows rows(p, s.expert, i0 + (lane >> 2));
   const int64_t tokens = min(p.T - t0, (int64_t)kMoeTokens);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + t0 * p.H, (uint32_t)(tokens * p.H * 2));
   uint16_t* h = p.h + t0 * p.top_k * p.I + i0;
@@ -423,19 +421,19 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(M
     const int slot = s.slots[min(c0 + r, s.n - 1)];
     const uint32_t row = (uint32_t)(slot / p.top_k) * (uint32_t)(p.H * 2);
     WeightUnit w[2];
-    ActUnit x;
+    ActUnit x = {};
     floatx4 acc[2][1];
     acc[0][0] = acc[1][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int u = wave; u < nu; u += NW) {
-      rows.load(w, u, nb, q);
-      load_acts(x, rx, row, u, nb, q);
+      rows.load(w, u, nb, lane);
+      load_acts(x, rx, c0 + r < s.n, row, u, nb, q);
       __builtin_amdgcn_sched_barrier(0);
       if (unit_cut(u, nb)) {
-        clear_unit(w[0], u, nb, q);
-        clear_unit(w[1], u, nb, q);
-        clear_acts(x, u, nb);
+        clear_unit(w[0], u, nb, lane);
+        clear_unit(w[1], u, nb, lane);
+        clear_acts(x, u, nb, q);
       }
-      multiply_unit<2, 1>(acc, w, [&](int b, int) { return x.x[b]; });
+      multiply_unit<2, 1>(acc, w, lane, [&](int i, int) { return x.x[i]; });
     }
     __syncthreads();
     part[wave][0][lane] = acc[0][0];
@@ -491,7 +489,7 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
       }
   };
   WeightUnit cur[2], nxt[2];
-  if (mine) rows.load(cur, 0, nb, q);
+  if (mine) rows.load(cur, 0, nb, lane);
   stage(0, 0);
   floatx4 acc[2][kT];
 #pragma unroll
@@ -501,16 +499,17 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
     __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     if (u + 1 < nu) {
-      if (mine) rows.load(nxt, u + 1, nb, q);
+      if (mine) rows.load(nxt, u + 1, nb, lane);
       if (kBufs == 2) stage(u + 1, buf ^ 1);
     }
     if (mine) {
       if (unit_cut(u, nb)) {
-        clear_unit(cur[0], u, nb, q);
-        clear_unit(cur[1], u, nb, q);
+        clear_unit(cur[0], u, nb, lane);
+        clear_unit(cur[1], u, nb, lane);
       }
-      multiply_unit<2, kT>(acc, cur, [&](int b, int t) {
-        return *(const u32x4*)&lds[buf * kBytes + (16 * t + r) * 1024 + 16 * ((4 * b + q) ^ r)];
+      multiply_unit<2, kT>(acc, cur, lane, [&](int i, int t) {
+        const int chunk = 16 * (i >> 2) + 4 * q + (i & 3);  // of block 4 (i / 4) + q, its 16 bytes i % 4
+        return *(const u32x4*)&lds[buf * kBytes + (16 * t + r) * 1024 + 16 * (chunk ^ r)];
       });
     }
     if (kBufs == 1 && u + 1 < nu) {
@@ -537,7 +536,7 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProb
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t i0 = (int64_t)blockIdx.x * (16 * kGateWaves) + 16 * wave, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const bool mine = i0 < p.I;  // I % 32 == 0: a wave's 16 rows are all there or none
-  const GateRows rows(p, s.expert, mine ? i0 + (lane & 15) : 0);
+  const GateRows rows(p, s.expert, mine ? i0 + (lane >> 2) : 0);
   if (s.n <= 16) gate_up_tiles<1>(p, s, rows, mine, t0, i0, wave, lane, lds);
   else if (s.n <= 32) gate_up_tiles<2>(p, s, rows, mine, t0, i0, wave, lane, lds);
   else gate_up_tiles<4>(p, s, rows, mine, t0, i0, wave, lane, lds);
@@ -571,27 +570,27 @@ __global__ void __launch_bounds__(512, 2) moe_down_kernel(MoeProblem p) {
   __syncthreads();
   const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.h + t0 * p.top_k * p.I, (uint32_t)(n * p.I * 2));
   const float* weights = p.weights + t0 * p.top_k;
-  const uint8_t* scales_end = p.w2_scales + (int64_t)p.E * p.H * nb;
   const int pairs = active * nu;
   WeightUnit cur[1], nxt[1];
   auto load = [&](WeightUnit& w, int at) {
-    const int64_t row = (int64_t)s_expert[at / nu] * p.H + o0 + r;
-    load_unit(w, p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb, scales_end, at % nu, nb, q);
+    const int64_t row = (int64_t)s_expert[at / nu] * p.H + o0 + (lane >> 2);
+    load_unit(w, p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb, at % nu, nb, lane);
   };
+  ActUnit x = {};
   if (wave < pairs) load(cur[0], wave);
   for (int at = wave; at < pairs; at += NW) {
     const int a = at / nu, u = at % nu, s0 = s_first[a], ns = s_first[a + 1] - s0;
-    ActUnit x;
-    load_acts(x, rh, (uint32_t)s_slot[s0 + min(r, ns - 1)] * (uint32_t)(p.I * 2), u, nb, q);
+    load_acts(x, rh, r < ns, (uint32_t)s_slot[s0 + min(r, ns - 1)] * (uint32_t)(p.I * 2), u, nb, q);
     if (at + NW < pairs) load(nxt[0], at + NW);
     __builtin_amdgcn_sched_barrier(0);
-    if (unit_cut(u, nb)) clear_unit(cur[0], u, nb, q);
+    if (unit_cut(u, nb)) clear_unit(cur[0], u, nb, lane);
     for (int c0 = 0; c0 < ns; c0 += 16) {
-      if (c0 > 0) load_acts(x, rh, (uint32_t)s_slot[s0 + min(c0 + r, ns - 1)] * (uint32_t)(p.I * 2), u, nb, q);
-      if (unit_cut(u, nb)) clear_acts(x, u, nb);
+      if (c0 > 0)
+        load_acts(x, rh, c0 + r < ns, (uint32_t)s_slot[s0 + min(c0 + r, ns - 1)] * (uint32_t)(p.I * 2), u, nb, q);
+      if (unit_cut(u, nb)) clear_acts(x, u, nb, q);
       floatx4 acc[1][1];
       acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-      multiply_unit<1, 1>(acc, cur, [&](int b, int) { return x.x[b]; });
+      multiply_unit<1, 1>(acc, cur, lane, [&](int i, int) { return x.x[i]; });
       if (c0 + r < ns) {
         const int slot = s_slot[s0 + c0 + r];
         sums[wave][slot / p.top_k][q] += weights[slot] * acc[0][0];
