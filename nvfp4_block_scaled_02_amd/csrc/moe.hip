@@ -106,8 +106,22 @@ struct MoePlan {
   int active;                      // experts reached
   int expert[kMoeExperts];         // their indices, increasing
   int first[kMoeExperts + 1];      // their first entry in slot[]
+  int tile[kMoeExperts];           // and their first tile of h
   int slot[kMoeSlots];
 };
+
+// h, between the two products, is kept in tiles of 16 slots of one expert, in the order in which
+// the second product's lanes take it: [tile][16-byte chunk of I][slot of the tile][16 bytes], so
+// that a load reads the slots' chunks side by side. (With a row per slot its loads, an access
+// for every lane, bounded that product: 64 tokens 81 us against 63.) Tiles that a chunk of
+// tokens can need: one per expert reached and one more per 16 slots.
+__host__ __device__ inline int64_t moe_tiles(int64_t slots, int64_t E) {
+  return (slots < E ? slots : E) + slots / 16;
+}
+__device__ __forceinline__ uint8_t* h_tiles(const MoeProblem& p) {
+  const int64_t tokens = min(p.T, (int64_t)kMoeTokens);
+  return (uint8_t*)p.h + (int64_t)blockIdx.z * moe_tiles(tokens * p.top_k, p.E) * (32 * p.I);
+}
 
 // Order of two logits as an unsigned key: increasing with the value, NaN above +inf, and
 // -inf at 0 (never chosen). key_logit is its inverse.
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
   if (e >= 0) atomicAdd(&count[e], 1);
   __syncthreads();
   if (wave == 0) {
-    int active = 0, first = 0;
+    int active = 0, first = 0, tile = 0;
     for (int b = 0; b < p.E; b += 64) {
       const int c = b + lane < p.E ? count[b + lane] : 0;
       const uint64_t on = __ballot(c > 0);
@@ -206,13 +220,22 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
         const int o = __shfl_up(sum, off, 64);
         if (lane >= off) sum += o;
       }
+      const int ct = (c + 15) >> 4;
+      int tiles = ct;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(tiles, off, 64);
+        if (lane >= off) tiles += o;
+      }
       if (b + lane < p.E) place[b + lane] = first + sum - c;
       if (c > 0) {
         plan->expert[rank] = b + lane;
         plan->first[rank] = first + sum - c;
+        plan->tile[rank] = tile + tiles - ct;
       }
       active += __popcll(on);
       first += __shfl(sum, 63, 64);
+      tile += __shfl(tiles, 63, 64);
     }
     if (lane == 0) {
       plan->active = active;
@@ -251,19 +274,34 @@ __device__ __forceinline__ bool unit_cut(int u, int nb) { return kUnit * u + kUn
 // Whether block b (of the row) is one that unit u multiplies.
 __device__ __forceinline__ bool unit_has(int u, int b, int nb) { return b >= kUnit * u && b < nb; }
 
-__device__ __forceinline__ void load_unit(WeightUnit& w, const uint8_t* codes, const uint8_t* scales, int u,
+// Where 16 rows start (the same for the whole wave), and this lane's share of them.
+struct WeightRows {
+  const uint8_t *codes, *scales;
+};
+struct WeightLane {
+  uint32_t codes, scales;
+  __device__ __forceinline__ WeightLane(int nb, int lane)
+      : codes((uint32_t)(lane >> 2) * (16u * (uint32_t)nb) + 16u * (uint32_t)(lane & 3)),
+        scales((uint32_t)(lane >> 2) * (uint32_t)nb + 4u * (uint32_t)(lane & 3)) {}
+};
+__device__ __forceinline__ void load_unit(WeightUnit& w, const WeightRows& rows, const WeightLane& at, int u,
                                           int nb, int lane) {
-  const int b0 = unit_start(u, nb), part = lane & 3;
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-    w.codes[g] = *(const u32x4*)&codes[16 * (uint32_t)min(b0 + 4 * g + part, nb - 1)];
+  const int b0 = unit_start(u, nb);
+  const uint8_t* codes = rows.codes + 16 * (int64_t)b0;
+  const uint8_t* scales = rows.scales + b0;
   if (nb >= kUnit) {
-    __builtin_memcpy(&w.scales, scales + b0 + 4 * part, 4);  // at any alignment
-  } else {
-    uint32_t s = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s |= (uint32_t)scales[min(4 * part + i, nb - 1)] << (8 * i);
-    w.scales = s;
+    for (int g = 0; g < 4; ++g) w.codes[g] = *(const u32x4*)&codes[at.codes + 64u * (uint32_t)g];
+    __builtin_memcpy(&w.scales, &scales[at.scales], 4);  // at any alignment
+  } else {  // a short row: its last block and byte for those it has not
+    const int part = lane & 3;
+    const uint32_t row = (uint32_t)(lane >> 2) * (uint32_t)nb;
+    w.scales = 0u;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      w.codes[g] = *(const u32x4*)&codes[16u * (row + (uint32_t)min(4 * g + part, nb - 1))];
+      w.scales |= (uint32_t)scales[row + (uint32_t)min(4 * part + g, nb - 1)] << (8 * g);
+    }
   }
 }
 // Codes and scale bytes of blocks that are not unit u's: zero.
@@ -278,21 +316,22 @@ __device__ __forceinline__ void clear_unit(WeightUnit& w, int u, int nb, int lan
 }
 
 // A unit's activations of 16 columns: lane (q, r) holds, of column r, elements 8j .. 8j + 7 of
-// block 4g + q in x[4 g + j]. The column's row starts at byte `row` of the window. What a short
-// row has no blocks for is read from beyond it (zeros past the window) and cleared. Lanes of
-// columns that are not there (`have` false) load nothing: a column's results depend on its own
-// activations alone.
+// block 4g + q in x[4 g + j]. load_acts: the column starts at byte `at` of the window and its
+// 16-byte chunks are `stride` bytes apart. What a short row has no blocks for is read from
+// beyond it (zeros past the window) and cleared. Lanes of columns that are not there (`have`
+// false) load nothing: a column's results depend on its own activations alone.
 struct ActUnit {
   u32x4 x[kUnit];
 };
-__device__ __forceinline__ void load_acts(ActUnit& a, __amdgpu_buffer_rsrc_t window, bool have, uint32_t row,
+template <int kStride>
+__device__ __forceinline__ void load_acts(ActUnit& a, __amdgpu_buffer_rsrc_t window, bool have, uint32_t at,
                                           int u, int nb, int q) {
   if (!have) return;
-  const uint32_t at = row + 64u * (uint32_t)(unit_start(u, nb) + q);
+  at += (uint32_t)(4 * kStride) * (uint32_t)(unit_start(u, nb) + q);
 #pragma unroll
   for (int i = 0; i < kUnit; ++i)
     a.x[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-        window, (int)(at + 256u * (uint32_t)(i >> 2) + 16u * (uint32_t)(i & 3)), 0, 0));
+        window, (int)(at + (uint32_t)kStride * (uint32_t)(16 * (i >> 2) + (i & 3))), 0, 0));
 }
 __device__ __forceinline__ void clear_acts(ActUnit& a, int u, int nb, int q) {
   const int b0 = unit_start(u, nb);
@@ -357,15 +396,6 @@ __device__ __forceinline__ void multiply_unit(floatx4 (&acc)[kF][kT], const Weig
   }
 }
 
-// silu(g) * u of four rows, as bf16: h is rounded to the type of the activations that the next
-// product takes.
-__device__ __forceinline__ u32x2 gated(const floatx4 g, const floatx4 u) {
-  float v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
-  return bf16x4_rne(v[0], v[1], v[2], v[3]);
-}
-
 constexpr int kTiles = kMoeTokens / 16;
 constexpr int kGateWaves = 4;
 
@@ -374,31 +404,45 @@ struct ExpertSlots {
   int64_t expert;
   const int* slots;
   int n;
+  uint8_t* h;  // its first tile
 };
 __device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s) {
   const MoePlan* plan = (const MoePlan*)p.plan + blockIdx.z;
   const int a = blockIdx.y;
-  s.expert = plan->expert[a];  // (of no meaning past the active ones, but in the buffer)
+  s.expert = __builtin_amdgcn_readfirstlane(plan->expert[a]);  // (of no meaning past the active ones, but in the buffer)
   s.slots = plan->slot + plan->first[a];
   s.n = plan->first[a + 1] - plan->first[a];
+  s.h = h_tiles(p) + (int64_t)plan->tile[a] * (32 * p.I);
   return a < plan->active;
 }
 
-// The gate and up rows that this lane loads of (row lane / 4 of 16).
+// 16 gate rows from row i of an expert on, and their up rows.
 struct GateRows {
-  const uint8_t *gate, *up, *gate_scales, *up_scales;
+  WeightRows gate, up;
   __device__ __forceinline__ GateRows(const MoeProblem& p, int64_t expert, int64_t i) {
-    const int64_t grow = expert * 2 * p.I + i, urow = grow + p.I;
-    gate = p.w13_packed + grow * (p.H >> 1);
-    up = p.w13_packed + urow * (p.H >> 1);
-    gate_scales = p.w13_scales + grow * (p.H >> 5);
-    up_scales = p.w13_scales + urow * (p.H >> 5);
+    const int64_t row = expert * 2 * p.I + i;
+    gate = WeightRows{p.w13_packed + row * (p.H >> 1), p.w13_scales + row * (p.H >> 5)};
+    up = WeightRows{gate.codes + p.I * (p.H >> 1), gate.scales + p.I * (p.H >> 5)};
   }
-  __device__ __forceinline__ void load(WeightUnit (&w)[2], int u, int nb, int lane) const {
-    load_unit(w[0], gate, gate_scales, u, nb, lane);
-    load_unit(w[1], up, up_scales, u, nb, lane);
+  __device__ __forceinline__ void load(WeightUnit (&w)[2], const WeightLane& at, int u, int nb, int lane) const {
+    load_unit(w[0], gate, at, u, nb, lane);
+    load_unit(w[1], up, at, u, nb, lane);
   }
 };
+
+// Where tile t of an expert keeps its slot r's elements i .. i + 3 (i a multiple of 4).
+__device__ __forceinline__ u32x2* h_place(const MoeProblem& p, const ExpertSlots& s, int t, int r, int64_t i) {
+  return (u32x2*)(s.h + (int64_t)t * (32 * p.I) + ((i >> 3) * 16 + r) * 16 + 2 * (i & 7));
+}
+
+// silu(g) * u of four rows, as bf16: h is rounded to the type of the activations that the next
+// product takes.
+__device__ __forceinline__ u32x2 gated(const floatx4 g, const floatx4 u) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
+  return bf16x4_rne(v[0], v[1], v[2], v[3]);
+}
 
 // h[slot, i] = silu(gate) * up, few experts reached: 16 gate rows and their up rows per
 // workgroup, whose waves take units of K in turn, a unit's weights and activations in flight at
@@ -413,10 +457,10 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(M
   const int q = lane >> 4, r = lane & 15;
   const int64_t i0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const int nb = (int)(p.H >> 5), nu = (nb + kUnit - 1) / kUnit;
-  const GateRows rows(p, s.expert, i0 + (lane >> 2));
+  const GateRows rows(p, s.expert, i0);
+  const WeightLane at(nb, lane);
   const int64_t tokens = min(p.T - t0, (int64_t)kMoeTokens);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + t0 * p.H, (uint32_t)(tokens * p.H * 2));
-  uint16_t* h = p.h + t0 * p.top_k * p.I + i0;
   for (int c0 = 0; c0 < s.n; c0 += 16) {
     const int slot = s.slots[min(c0 + r, s.n - 1)];
     const uint32_t row = (uint32_t)(slot / p.top_k) * (uint32_t)(p.H * 2);
@@ -425,8 +469,8 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(M
     floatx4 acc[2][1];
     acc[0][0] = acc[1][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int u = wave; u < nu; u += NW) {
-      rows.load(w, u, nb, lane);
-      load_acts(x, rx, c0 + r < s.n, row, u, nb, q);
+      rows.load(w, at, u, nb, lane);
+      load_acts<16>(x, rx, c0 + r < s.n, row, u, nb, q);
       __builtin_amdgcn_sched_barrier(0);
       if (unit_cut(u, nb)) {
         clear_unit(w[0], u, nb, lane);
@@ -446,7 +490,7 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(M
         g += part[w][0][lane];
         v += part[w][1][lane];
       }
-      *(u32x2*)&h[(uint32_t)slot * (uint32_t)p.I + 4 * q] = gated(g, v);
+      *h_place(p, s, c0 >> 4, r, i0 + 4 * q) = gated(g, v);
     }
   }
 }
@@ -466,15 +510,12 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
   const int nb = (int)(p.H >> 5), nu = (nb + kUnit - 1) / kUnit;
   const int64_t tokens = min(p.T - t0, (int64_t)kMoeTokens);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + t0 * p.H, (uint32_t)(tokens * p.H * 2));
-  int slot[kT];      // of this lane's columns
-  uint32_t row0[kT];  // and where their activations start
+  uint32_t row0[kT];  // where the activations of this lane's columns start
 #pragma unroll
-  for (int t = 0; t < kT; ++t) {
-    slot[t] = s.slots[min(16 * t + r, s.n - 1)];
-    row0[t] = (uint32_t)(slot[t] / p.top_k) * (uint32_t)(p.H * 2);
-  }
+  for (int t = 0; t < kT; ++t)
+    row0[t] = (uint32_t)(s.slots[min(16 * t + r, s.n - 1)] / p.top_k) * (uint32_t)(p.H * 2);
   auto stage = [&](int u, int buf) {
-    const uint32_t at = (uint32_t)unit_start(u, nb) * 64u;
+    const uint32_t from = (uint32_t)unit_start(u, nb) * 64u;
 #pragma unroll
     for (int t = 0; t < kT; ++t)
 #pragma unroll
@@ -485,11 +526,12 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
         // blocks that are not the unit's lie past the window: zeros
         const uint32_t past = unit_has(u, unit_start(u, nb) + (chunk >> 2), nb) ? 0u : 0x80000000u;
         const uint32_t start = (uint32_t)__builtin_amdgcn_readlane((int)row0[t], row);
-        buffer_load_lds16(rx, lds + buf * kBytes + (16 * t + row) * 1024, (start + 16u * (uint32_t)chunk) | past, at);
+        buffer_load_lds16(rx, lds + buf * kBytes + (16 * t + row) * 1024, (start + 16u * (uint32_t)chunk) | past, from);
       }
   };
+  const WeightLane at(nb, lane);
   WeightUnit cur[2], nxt[2];
-  if (mine) rows.load(cur, 0, nb, lane);
+  if (mine) rows.load(cur, at, 0, nb, lane);
   stage(0, 0);
   floatx4 acc[2][kT];
 #pragma unroll
@@ -499,7 +541,7 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
     __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     if (u + 1 < nu) {
-      if (mine) rows.load(nxt, u + 1, nb, lane);
+      if (mine) rows.load(nxt, at, u + 1, nb, lane);
       if (kBufs == 2) stage(u + 1, buf ^ 1);
     }
     if (mine) {
@@ -521,11 +563,9 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
     cur[1] = nxt[1];
   }
   if (!mine) return;
-  uint16_t* h = p.h + t0 * p.top_k * p.I + i0;
 #pragma unroll
   for (int t = 0; t < kT; ++t)
-    if (16 * t + r < s.n)
-      *(u32x2*)&h[(uint32_t)slot[t] * (uint32_t)p.I + 4 * q] = gated(acc[0][t], acc[1][t]);
+    if (16 * t + r < s.n) *h_place(p, s, t, r, i0 + 4 * q) = gated(acc[0][t], acc[1][t]);
 }
 
 __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProblem p) {
@@ -536,7 +576,7 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProb
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t i0 = (int64_t)blockIdx.x * (16 * kGateWaves) + 16 * wave, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const bool mine = i0 < p.I;  // I % 32 == 0: a wave's 16 rows are all there or none
-  const GateRows rows(p, s.expert, mine ? i0 + (lane >> 2) : 0);
+  const GateRows rows(p, s.expert, mine ? i0 : 0);
   if (s.n <= 16) gate_up_tiles<1>(p, s, rows, mine, t0, i0, wave, lane, lds);
   else if (s.n <= 32) gate_up_tiles<2>(p, s, rows, mine, t0, i0, wave, lane, lds);
   else gate_up_tiles<4>(p, s, rows, mine, t0, i0, wave, lane, lds);
@@ -545,11 +585,12 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProb
 // out[t, o] for 16 rows of W2 and one chunk of tokens: the workgroup's waves take (expert,
 // unit of K) pairs in turn, each with its next pair's weights in flight, and add the weighted results to their own fp32 sums by token in LDS; the waves' sums
 // are added in a fixed order.
-__global__ void __launch_bounds__(512, 2) moe_down_kernel(MoeProblem p) {
-  constexpr int NW = 8;
+__global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
+  constexpr int NW = 16;
   __shared__ floatx4 sums[NW][kMoeTokens][4];
   __shared__ int s_expert[kMoeExperts];
   __shared__ int s_first[kMoeExperts + 1];
+  __shared__ int s_tile[kMoeExperts];
   __shared__ int s_slot[kMoeSlots];
   const MoePlan* plan = (const MoePlan*)p.plan + blockIdx.z;
   const int lane = threadIdx.x & 63;
@@ -562,31 +603,52 @@ __global__ void __launch_bounds__(512, 2) moe_down_kernel(MoeProblem p) {
   const int n = nt * p.top_k, most = min(n, p.E);
   const int active = plan->active;
   // the plan's lists, as long as they can be (past the active experts: of no meaning)
-  for (int i = threadIdx.x; i < most; i += 64 * NW) s_expert[i] = plan->expert[i];
+  for (int i = threadIdx.x; i < most; i += 64 * NW) {
+    s_expert[i] = plan->expert[i];
+    s_tile[i] = plan->tile[i];
+  }
   for (int i = threadIdx.x; i <= most; i += 64 * NW) s_first[i] = plan->first[i];
   for (int i = threadIdx.x; i < n; i += 64 * NW) s_slot[i] = plan->slot[i];
   for (int i = threadIdx.x; i < NW * nt * 4; i += 64 * NW)
     sums[i / (nt * 4)][i % (nt * 4) >> 2][i & 3] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
-  const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.h + t0 * p.top_k * p.I, (uint32_t)(n * p.I * 2));
+  uint8_t* h = h_tiles(p);
   const float* weights = p.weights + t0 * p.top_k;
-  const int pairs = active * nu;
-  WeightUnit cur[1], nxt[1];
-  auto load = [&](WeightUnit& w, int at) {
-    const int64_t row = (int64_t)s_expert[at / nu] * p.H + o0 + (lane >> 2);
-    load_unit(w, p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb, at % nu, nb, lane);
+  const WeightLane lane_at(nb, lane);
+  // pair (a, u): unit u of the a-th expert; a wave's next is NW units on
+  struct Pair {
+    int a, u;
   };
+  auto next = [&](Pair k) {
+    k.u += NW;
+    while (k.u >= nu) {
+      k.u -= nu;
+      ++k.a;
+    }
+    return k;
+  };
+  auto load = [&](WeightUnit& w, const Pair& k) {
+    const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(s_expert[k.a]) * p.H + o0;
+    load_unit(w, WeightRows{p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb}, lane_at, k.u, nb, lane);
+  };
+  WeightUnit cur[1];
   ActUnit x = {};
-  if (wave < pairs) load(cur[0], wave);
-  for (int at = wave; at < pairs; at += NW) {
-    const int a = at / nu, u = at % nu, s0 = s_first[a], ns = s_first[a + 1] - s0;
-    load_acts(x, rh, r < ns, (uint32_t)s_slot[s0 + min(r, ns - 1)] * (uint32_t)(p.I * 2), u, nb, q);
-    if (at + NW < pairs) load(nxt[0], at + NW);
+  Pair at = next(Pair{0, wave - NW});
+  while (at.a < active) {
+    const int s0 = __builtin_amdgcn_readfirstlane(s_first[at.a]);
+    const int ns = __builtin_amdgcn_readfirstlane(s_first[at.a + 1]) - s0, u = at.u;
+    const uint8_t* tiles = h + (int64_t)__builtin_amdgcn_readfirstlane(s_tile[at.a]) * (32 * p.I);
+    auto load_tile = [&](int c0) {
+      load_acts<256>(x, make_rsrc(tiles + (int64_t)(c0 >> 4) * (32 * p.I), (uint32_t)(32 * p.I)), c0 + r < ns,
+                     16u * (uint32_t)r, u, nb, q);
+    };
+    load_tile(0);
+    load(cur[0], at);
+    at = next(at);
     __builtin_amdgcn_sched_barrier(0);
     if (unit_cut(u, nb)) clear_unit(cur[0], u, nb, lane);
     for (int c0 = 0; c0 < ns; c0 += 16) {
-      if (c0 > 0)
-        load_acts(x, rh, c0 + r < ns, (uint32_t)s_slot[s0 + min(c0 + r, ns - 1)] * (uint32_t)(p.I * 2), u, nb, q);
+      if (c0 > 0) load_tile(c0);
       if (unit_cut(u, nb)) clear_acts(x, u, nb, q);
       floatx4 acc[1][1];
       acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -596,7 +658,6 @@ __global__ void __launch_bounds__(512, 2) moe_down_kernel(MoeProblem p) {
         sums[wave][slot / p.top_k][q] += weights[slot] * acc[0][0];
       }
     }
-    cur[0] = nxt[0];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < nt * 4; i += 64 * NW) {
@@ -612,6 +673,11 @@ __global__ void __launch_bounds__(512, 2) moe_down_kernel(MoeProblem p) {
 
 int64_t moe_plan_bytes(int64_t T) {
   return (T + kMoeTokens - 1) / kMoeTokens * (int64_t)sizeof(MoePlan);
+}
+
+int64_t moe_h_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k) {
+  const int64_t tokens = T < kMoeTokens ? T : kMoeTokens;
+  return (T + kMoeTokens - 1) / kMoeTokens * moe_tiles(tokens * top_k, E) * (32 * I);
 }
 
 hipError_t launch_moe_router(const void* x, const void* w, int64_t T, int64_t E, int64_t H,
@@ -642,7 +708,7 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
                        dim3(64 * kGateWaves), 0, stream, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16), 1, chunks), dim3(512), 0, stream, p);
+  hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16), 1, chunks), dim3(1024), 0, stream, p);
   return hipGetLastError();
 }
 
