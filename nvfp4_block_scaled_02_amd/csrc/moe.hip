@@ -583,8 +583,8 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProb
 }
 
 // out[t, o] for 16 rows of W2 and one chunk of tokens: the workgroup's waves take (expert,
-// unit of K) pairs in turn, each with its next pair's weights in flight, and add the weighted results to their own fp32 sums by token in LDS; the waves' sums
-// are added in a fixed order.
+// unit of K) pairs in turn, a pair's weights and h in flight at once, and add the weighted
+// results to their own fp32 sums by token in LDS; the waves' sums are added in a fixed order.
 __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
   constexpr int NW = 16;
   __shared__ floatx4 sums[NW][kMoeTokens][4];

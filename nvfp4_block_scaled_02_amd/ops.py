@@ -12,6 +12,7 @@ import ctypes
 
 import torch
 
+from . import _lib
 from ._lib import check, load_library
 
 
@@ -187,37 +188,52 @@ def mxfp8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Ten
     return out
 
 
-def _one_device(*tensors) -> torch.device:
-    """The device that all the tensors are on."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"tensors are on different devices: {dev} and {t.device}")
-    return dev
+# The calls below are made once per layer for a single token, where the host's part of a call
+# is as long as the kernel: their checks are one expression per tensor that falls back to _need
+# (and its messages) only when something is wrong, pointers go to the library as integers, and
+# the stream's handle is asked of PyTorch directly.
+
+
+def _want(t: torch.Tensor, name: str, dtype, ndim: int, index: int | None = None):
+    """_need, and the tensor on device ``index``."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.ndim != ndim or not t.is_cuda \
+            or not t.is_contiguous():
+        _need(t, name, dtype, ndim)
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{index}")
+
+
+def _library():
+    return _lib._lib or load_library()
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 @contextlib.contextmanager
-def _place(dev: torch.device, stream):
+def _place(index: int, stream):
     """The device and the stream that a call launches and allocates on, as PyTorch's current
     ones: what the call allocates then belongs to the stream that uses it."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
         yield
 
 
-def _elsewhere(dev: torch.device, stream) -> bool:
+def _elsewhere(index: int, stream) -> bool:
     """Whether a call has to change PyTorch's current device or stream."""
-    return stream is not None or dev.index != torch.cuda.current_device()
+    return stream is not None or index != torch.cuda.current_device()
 
 
 def mxfp4_quantize(x: torch.Tensor, packed: torch.Tensor | None = None,
                    scales: torch.Tensor | None = None, stream=None):
     """MXFP4 quantization: bf16 [M, K] -> packed E2M1 uint8 [M, K/2] + E8M0 scales
     [M, K/32]. A block with a NaN or an infinity becomes a NaN block (scale byte 0xFF)."""
-    _need(x, "x", torch.bfloat16, 2)
-    if _elsewhere(x.device, stream):
-        with _place(x.device, stream):
+    _want(x, "x", torch.bfloat16, 2)
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
             return mxfp4_quantize(x, packed, scales)
     M, K = x.shape
     if K % 32:
@@ -226,48 +242,49 @@ def mxfp4_quantize(x: torch.Tensor, packed: torch.Tensor | None = None,
         packed = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
     if scales is None:
         scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-    _need(packed, "packed", torch.uint8, 2)
-    _need(scales, "scales", torch.uint8, 2)
+    _want(packed, "packed", torch.uint8, 2, dev)
+    _want(scales, "scales", torch.uint8, 2, dev)
     if packed.shape != (M, K // 2) or scales.shape != (M, K // 32):
         raise ValueError("packed must be [M, K/2] and scales [M, K/32]")
-    _one_device(x, packed, scales)
     if M:
-        check(load_library().nvfp4_mxfp4_quantize(_ptr(x), M, K, _ptr(packed), _ptr(scales), _stream()),
-              "nvfp4_mxfp4_quantize")
+        check(_library().nvfp4_mxfp4_quantize(x.data_ptr(), M, K, packed.data_ptr(), scales.data_ptr(),
+                                              _raw_stream(dev)), "nvfp4_mxfp4_quantize")
     return packed, scales
 
 
 def mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None,
                      stream=None) -> torch.Tensor:
     """The values of an MXFP4 tensor as bf16 [M, K]."""
-    _need(packed, "packed", torch.uint8, 2)
-    _need(scales, "scales", torch.uint8, 2)
-    if _elsewhere(packed.device, stream):
-        with _place(packed.device, stream):
+    _want(packed, "packed", torch.uint8, 2)
+    dev = packed.get_device()
+    _want(scales, "scales", torch.uint8, 2, dev)
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
             return mxfp4_dequantize(packed, scales, out)
     M, K = packed.shape[0], 2 * packed.shape[1]
     if K % 32 or scales.shape != (M, K // 32):
         raise ValueError("packed must be [M, K/2] and scales [M, K/32], K a multiple of 32")
     if out is None:
         out = torch.empty((M, K), dtype=torch.bfloat16, device=packed.device)
-    _need(out, "out", torch.bfloat16, 2)
+    _want(out, "out", torch.bfloat16, 2, dev)
     if out.shape != (M, K):
         raise ValueError("out shape must be [M, K]")
-    _one_device(packed, scales, out)
     if M:
-        check(load_library().nvfp4_mxfp4_dequantize(_ptr(packed), _ptr(scales), M, K, _ptr(out), _stream()),
-              "nvfp4_mxfp4_dequantize")
+        check(_library().nvfp4_mxfp4_dequantize(packed.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(),
+                                                _raw_stream(dev)), "nvfp4_mxfp4_dequantize")
     return out
 
 
 def mxfp4_gemm(a_packed: torch.Tensor, a_scales: torch.Tensor, w_packed: torch.Tensor,
                w_scales: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """MXFP4 GEMM: bf16 [M, N] = A_hat @ W_hat^T on the block-scaled fp4 MFMA."""
-    for t, n in ((a_packed, "a_packed"), (a_scales, "a_scales"), (w_packed, "w_packed"),
-                 (w_scales, "w_scales")):
-        _need(t, n, torch.uint8, 2)
-    if _elsewhere(a_packed.device, stream):
-        with _place(a_packed.device, stream):
+    _want(a_packed, "a_packed", torch.uint8, 2)
+    dev = a_packed.get_device()
+    _want(a_scales, "a_scales", torch.uint8, 2, dev)
+    _want(w_packed, "w_packed", torch.uint8, 2, dev)
+    _want(w_scales, "w_scales", torch.uint8, 2, dev)
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
             return mxfp4_gemm(a_packed, a_scales, w_packed, w_scales, out)
     M, Kh = a_packed.shape
     N = w_packed.shape[0]
@@ -276,13 +293,12 @@ def mxfp4_gemm(a_packed: torch.Tensor, a_scales: torch.Tensor, w_packed: torch.T
         raise ValueError("operand shapes are inconsistent")
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a_packed.device)
-    _need(out, "out", torch.bfloat16, 2)
+    _want(out, "out", torch.bfloat16, 2, dev)
     if out.shape != (M, N):
         raise ValueError("out shape must be [M, N]")
-    _one_device(a_packed, a_scales, w_packed, w_scales, out)
     if M and N:
-        check(load_library().nvfp4_mxfp4_gemm(_ptr(a_packed), _ptr(a_scales), _ptr(w_packed),
-                                              _ptr(w_scales), M, N, K, _ptr(out), _stream()),
+        check(_library().nvfp4_mxfp4_gemm(a_packed.data_ptr(), a_scales.data_ptr(), w_packed.data_ptr(),
+                                          w_scales.data_ptr(), M, N, K, out.data_ptr(), _raw_stream(dev)),
               "nvfp4_mxfp4_gemm")
     return out
 
@@ -306,30 +322,30 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                  stream=None) -> torch.Tensor:
     """MXFP4 linear: quantize x, then the MXFP4 GEMM."""
-    _need(x, "x", torch.bfloat16, 2)
-    _need(w_packed, "w_packed", torch.uint8, 2)
-    _need(w_scales, "w_scales", torch.uint8, 2)
-    if _elsewhere(x.device, stream):
-        with _place(x.device, stream):
+    _want(x, "x", torch.bfloat16, 2)
+    dev = x.get_device()
+    _want(w_packed, "w_packed", torch.uint8, 2, dev)
+    _want(w_scales, "w_scales", torch.uint8, 2, dev)
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
             return mxfp4_linear(x, w_packed, w_scales, out, workspace)
     M, K = x.shape
     N = w_packed.shape[0]
     if w_packed.shape != (N, K // 2) or w_scales.shape != (N, K // 32):
         raise ValueError("weight shapes do not match x")
-    lib = load_library()
+    lib = _library()
     if workspace is None:
         need = lib.nvfp4_mxfp4_linear_workspace_bytes(M, K)
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
-    _need(workspace, "workspace", torch.uint8, 1)
+    _want(workspace, "workspace", torch.uint8, 1, dev)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    _need(out, "out", torch.bfloat16, 2)
+    _want(out, "out", torch.bfloat16, 2, dev)
     if out.shape != (M, N):
         raise ValueError("out shape must be [M, N]")
-    _one_device(x, w_packed, w_scales, workspace, out)
     if M and N:
-        check(lib.nvfp4_mxfp4_linear(_ptr(x), _ptr(w_packed), _ptr(w_scales), M, N, K, _ptr(out),
-                                     _ptr(workspace), workspace.numel(), _stream()),
+        check(lib.nvfp4_mxfp4_linear(x.data_ptr(), w_packed.data_ptr(), w_scales.data_ptr(), M, N, K,
+                                     out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)),
               "nvfp4_mxfp4_linear")
     return out
 
@@ -338,10 +354,11 @@ def moe_router(x: torch.Tensor, router: torch.Tensor, logits: torch.Tensor | Non
                stream=None) -> torch.Tensor:
     """Router logits of a mixture-of-experts layer: fp32 [T, E] = x @ router^T (x bf16 [T, H],
     router bf16 [E, H]), summed in fp64 and rounded once."""
-    _need(x, "x", torch.bfloat16, 2)
-    _need(router, "router", torch.bfloat16, 2)
-    if _elsewhere(x.device, stream):
-        with _place(x.device, stream):
+    _want(x, "x", torch.bfloat16, 2)
+    dev = x.get_device()
+    _want(router, "router", torch.bfloat16, 2, dev)
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
             return moe_router(x, router, logits)
     T, H = x.shape
     E = router.shape[0]
@@ -349,13 +366,12 @@ def moe_router(x: torch.Tensor, router: torch.Tensor, logits: torch.Tensor | Non
         raise ValueError("router must be [E, H]")
     if logits is None:
         logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
-    _need(logits, "logits", torch.float32, 2)
+    _want(logits, "logits", torch.float32, 2, dev)
     if logits.shape != (T, E):
         raise ValueError("logits shape must be [T, E]")
-    _one_device(x, router, logits)
     if T:
-        check(load_library().nvfp4_moe_router(_ptr(x), _ptr(router), T, E, H, _ptr(logits), _stream()),
-              "nvfp4_moe_router")
+        check(_library().nvfp4_moe_router(x.data_ptr(), router.data_ptr(), T, E, H, logits.data_ptr(),
+                                          _raw_stream(dev)), "nvfp4_moe_router")
     return logits
 
 
@@ -375,13 +391,15 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
     ``renormalize``: the chosen experts' weights sum to one (else their share of the softmax
     over all experts). With ``return_routing`` the result is ``(out, ids int32 [T, top_k],
     weights fp32 [T, top_k])``. A row of logits that are all -inf has output 0."""
-    _need(x, "x", torch.bfloat16, 2)
-    _need(logits, "logits", torch.float32, 2)
-    for t, n in ((w13_packed, "w13_packed"), (w13_scales, "w13_scales"), (w2_packed, "w2_packed"),
-                 (w2_scales, "w2_scales")):
-        _need(t, n, torch.uint8, 3)
-    if _elsewhere(x.device, stream):
-        with _place(x.device, stream):
+    _want(x, "x", torch.bfloat16, 2)
+    dev = x.get_device()
+    _want(logits, "logits", torch.float32, 2, dev)
+    _want(w13_packed, "w13_packed", torch.uint8, 3, dev)
+    _want(w13_scales, "w13_scales", torch.uint8, 3, dev)
+    _want(w2_packed, "w2_packed", torch.uint8, 3, dev)
+    _want(w2_scales, "w2_scales", torch.uint8, 3, dev)
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
             return mxfp4_moe(x, logits, w13_packed, w13_scales, w2_packed, w2_scales, top_k,
                              renormalize, out, workspace, return_routing)
     T, H = x.shape
@@ -390,29 +408,28 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
             w13_scales.shape != (E, 2 * I, H // 32) or w2_packed.shape != (E, H, I // 2) or \
             w2_scales.shape != (E, H, I // 32):
         raise ValueError("expert weight or logit shapes are inconsistent")
-    lib = load_library()
+    lib = _library()
     if workspace is None:
         need = lib.nvfp4_mxfp4_moe_workspace_bytes(T, E, I, top_k)
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
-    _need(workspace, "workspace", torch.uint8, 1)
+    _want(workspace, "workspace", torch.uint8, 1, dev)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    _need(out, "out", torch.bfloat16, 2)
+    _want(out, "out", torch.bfloat16, 2, dev)
     if out.shape != (T, H):
         raise ValueError("out shape must be [T, H]")
-    _one_device(x, logits, w13_packed, w13_scales, w2_packed, w2_scales, workspace, out)
     ids = weights = None
     if return_routing:
         n = max(int(top_k), 0)
         ids = torch.empty((T, n), dtype=torch.int32, device=x.device)
         weights = torch.empty((T, n), dtype=torch.float32, device=x.device)
     if T:
-        check(lib.nvfp4_mxfp4_moe(_ptr(x), _ptr(logits), _ptr(w13_packed), _ptr(w13_scales),
-                                  _ptr(w2_packed), _ptr(w2_scales), T, E, H, I, top_k,
-                                  int(bool(renormalize)), _ptr(out),
-                                  _ptr(ids) if return_routing else None,
-                                  _ptr(weights) if return_routing else None, _ptr(workspace),
-                                  workspace.numel(), _stream()), "nvfp4_mxfp4_moe")
+        check(lib.nvfp4_mxfp4_moe(x.data_ptr(), logits.data_ptr(), w13_packed.data_ptr(),
+                                  w13_scales.data_ptr(), w2_packed.data_ptr(), w2_scales.data_ptr(), T, E, H,
+                                  I, top_k, int(bool(renormalize)), out.data_ptr(),
+                                  ids.data_ptr() if return_routing else None,
+                                  weights.data_ptr() if return_routing else None, workspace.data_ptr(),
+                                  workspace.numel(), _raw_stream(dev)), "nvfp4_mxfp4_moe")
     return (out, ids, weights) if return_routing else out
 
 
