@@ -176,15 +176,32 @@ __device__ __forceinline__ Choice moe_topk(const float* __restrict__ row, int E,
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (64 * i < E && (uint32_t)(lane + 64 * i) == e) key[i] = 0u;
-    const float p = expf(key_logit(k) - top);
-    if (renormalize) sum += p;
-    if (lane == j) mine = Choice{(int)e, p};
+    if (lane == j) mine = Choice{(int)e, key_logit(k)};
   }
-  mine.weight = mine.id < 0 ? 0.0f : mine.weight / sum;
+  // the choices' exponentials at once, in the lanes that hold them
+  mine.weight = mine.id < 0 ? 0.0f : expf(mine.weight - top);
+  if (renormalize) sum = wave_sum(mine.weight);
+  if (mine.id >= 0) mine.weight /= sum;
   return mine;
 }
+__device__ __forceinline__ void route_token(const MoeProblem& p, int64_t t, int lane, int* chosen) {
+  const Choice c = moe_topk(p.logits + t * p.E, p.E, p.top_k, p.renormalize, lane);
+  if (lane < p.top_k) {
+    if (chosen) chosen[lane] = c.id;
+    p.ids[t * p.top_k + lane] = c.id;
+    p.weights[t * p.top_k + lane] = c.weight;
+  }
+}
 
-// One workgroup per chunk.
+// The routing of many tokens, a token per wave, over the whole chip: in the plan's one workgroup
+// the selection is bound by its instructions (64 tokens of 128 experts, 8 of each: 25 us).
+__global__ void __launch_bounds__(256) moe_route_kernel(MoeProblem p) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t < p.T) route_token(p, t, threadIdx.x & 63, nullptr);
+}
+
+// One workgroup per chunk; kRoute: it routes the tokens itself, one per wave.
+template <bool kRoute>
 __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
   __shared__ int count[kMoeExperts];
   __shared__ int place[kMoeExperts];
@@ -195,13 +212,10 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
   const int n = nt * p.top_k;
   MoePlan* plan = (MoePlan*)p.plan + blockIdx.x;
   for (int e = threadIdx.x; e < p.E; e += 1024) count[e] = 0;
-  for (int t = wave; t < nt; t += 16) {
-    const Choice c = moe_topk(p.logits + (t0 + t) * p.E, p.E, p.top_k, p.renormalize, lane);
-    if (lane < p.top_k) {
-      chosen[t * p.top_k + lane] = c.id;
-      p.ids[(t0 + t) * p.top_k + lane] = c.id;
-      p.weights[(t0 + t) * p.top_k + lane] = c.weight;
-    }
+  if constexpr (kRoute) {
+    if (wave < nt) route_token(p, t0 + wave, lane, chosen + wave * p.top_k);
+  } else {
+    for (int i = threadIdx.x; i < n; i += 1024) chosen[i] = p.ids[t0 * p.top_k + i];
   }
   __syncthreads();
   const int s = threadIdx.x;  // n <= 1024
@@ -416,6 +430,79 @@ __device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s
   return a < plan->active;
 }
 
+// The same without a plan made before, for one to four tokens: every workgroup routes all of
+// them, a token per wave, and orders their at most 64 slots in a wave's lanes; the first one
+// writes the plan for the second product. (One token: a launch and its 5 us less, for 1 us in
+// each workgroup.) With at most 16 tokens an expert has one tile of h.
+constexpr int kInlineTokens = 4;
+static_assert(kInlineTokens * kMoeTopK <= 64 && kInlineTokens <= kGateWaves, "a slot per lane, a token per wave");
+struct InlinePlan {
+  int id[64];
+  float weight[64];
+  int slot[kInlineTokens];
+};
+__device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s, InlinePlan& ip, int wave,
+                                             int lane) {
+  const int T = (int)p.T, n = T * p.top_k;
+  if (wave < T) {
+    const Choice c = moe_topk(p.logits + (int64_t)wave * p.E, p.E, p.top_k, p.renormalize, lane);
+    if (lane < p.top_k) {
+      ip.id[wave * p.top_k + lane] = c.id;
+      ip.weight[wave * p.top_k + lane] = c.weight;
+    }
+  }
+  __syncthreads();
+  const int id = lane < n ? ip.id[lane] : -1;
+  // of this lane's expert: its slots before this one; in all, slots and experts of lower index
+  int before = 0, slots_below = 0, experts_below = 0;
+  uint64_t firsts = 0;  // lanes that are their expert's first slot
+  for (int i = 0; i < n; ++i) {
+    const int o = __builtin_amdgcn_readlane(id, i);
+    if (o < 0) continue;
+    before += o == id && i < lane;
+    slots_below += o < id;
+  }
+  firsts = __ballot(id >= 0 && before == 0);
+  for (uint64_t f = firsts; f != 0; f &= f - 1) experts_below += __builtin_amdgcn_readlane(id, __builtin_ctzll(f)) < id;
+  const int active = __popcll(firsts), a = blockIdx.y;
+  if (blockIdx.x == 0 && a == 0 && wave == 0) {
+    MoePlan* plan = (MoePlan*)p.plan;
+    if (lane < n) {
+      p.ids[lane] = id;
+      p.weights[lane] = ip.weight[lane];
+    }
+    if (id >= 0) plan->slot[slots_below + before] = lane;
+    if (id >= 0 && before == 0) {
+      plan->expert[experts_below] = id;
+      plan->first[experts_below] = slots_below;
+      plan->tile[experts_below] = experts_below;
+    }
+    const int chosen = __popcll(__ballot(id >= 0));
+    if (lane == 0) {
+      plan->active = active;
+      plan->first[active] = chosen;
+    }
+  }
+  if (a >= active) return false;
+  const uint64_t mine = __ballot(id >= 0 && experts_below == a);
+  s.expert = __builtin_amdgcn_readlane(id, __builtin_ctzll(mine));
+  s.n = __popcll(mine);
+  if (wave == 0 && id >= 0 && experts_below == a) ip.slot[before] = lane;
+  __syncthreads();
+  s.slots = ip.slot;
+  s.h = h_tiles(p) + (int64_t)a * (32 * p.I);
+  return true;
+}
+template <bool kInline>
+__device__ __forceinline__ bool find_slots(const MoeProblem& p, ExpertSlots& s, int wave, int lane) {
+  if constexpr (kInline) {
+    __shared__ InlinePlan ip;
+    return expert_slots(p, s, ip, wave, lane);
+  } else {
+    return expert_slots(p, s);
+  }
+}
+
 // 16 gate rows from row i of an expert on, and their up rows.
 struct GateRows {
   WeightRows gate, up;
@@ -447,13 +534,14 @@ __device__ __forceinline__ u32x2 gated(const floatx4 g, const floatx4 u) {
 // h[slot, i] = silu(gate) * up, few experts reached: 16 gate rows and their up rows per
 // workgroup, whose waves take units of K in turn, a unit's weights and activations in flight at
 // once, and meet in LDS.
+template <bool kInline>
 __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(MoeProblem p) {
   constexpr int NW = kGateWaves;
   __shared__ floatx4 part[NW][2][64];
-  ExpertSlots s;
-  if (!expert_slots(p, s)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  ExpertSlots s;
+  if (!find_slots<kInline>(p, s, wave, lane)) return;
   const int q = lane >> 4, r = lane & 15;
   const int64_t i0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const int nb = (int)(p.H >> 5), nu = (nb + kUnit - 1) / kUnit;
@@ -568,12 +656,13 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
     if (16 * t + r < s.n) *h_place(p, s, t, r, i0 + 4 * q) = gated(acc[0][t], acc[1][t]);
 }
 
+template <bool kInline>
 __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProblem p) {
   __shared__ __align__(16) uint8_t lds[kTiles * 16 * 1024];
-  ExpertSlots s;
-  if (!expert_slots(p, s)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  ExpertSlots s;
+  if (!find_slots<kInline>(p, s, wave, lane)) return;
   const int64_t i0 = (int64_t)blockIdx.x * (16 * kGateWaves) + 16 * wave, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const bool mine = i0 < p.I;  // I % 32 == 0: a wave's 16 rows are all there or none
   const GateRows rows(p, s.expert, mine ? i0 : 0);
@@ -697,15 +786,30 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   const unsigned chunks = (unsigned)((p.T + kMoeTokens - 1) / kMoeTokens);
   const int64_t slots = (p.T < kMoeTokens ? p.T : kMoeTokens) * p.top_k;
   const unsigned most = (unsigned)(slots < p.E ? slots : p.E);  // experts a chunk can reach
-  hipLaunchKernelGGL(moe_plan_kernel, dim3(chunks), dim3(1024), 0, stream, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const unsigned wide = (unsigned)((p.I + 63) / 64);
-  if ((int64_t)wide * most * chunks >= 512)
-    hipLaunchKernelGGL(moe_gate_up_kernel, dim3(wide, most, chunks), dim3(64 * kGateWaves), 0, stream, p);
-  else
-    hipLaunchKernelGGL(moe_gate_up_split_kernel, dim3((unsigned)(p.I / 16), most, chunks),
-                       dim3(64 * kGateWaves), 0, stream, p);
+  const bool in_line = p.T <= kInlineTokens;
+  hipError_t e;
+  if (!in_line) {
+    if (p.T <= 16) {
+      hipLaunchKernelGGL(moe_plan_kernel<true>, dim3(1), dim3(1024), 0, stream, p);
+    } else {
+      hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((p.T + 3) / 4)), dim3(256), 0, stream, p);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(moe_plan_kernel<false>, dim3(chunks), dim3(1024), 0, stream, p);
+    }
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const dim3 wide((unsigned)((p.I + 63) / 64), most, chunks), narrow((unsigned)(p.I / 16), most, chunks);
+  const dim3 block(64 * kGateWaves);
+  // workgroups of 64 rows where they are two per compute unit of an MI355X, else of 16
+  if ((int64_t)wide.x * wide.y * wide.z >= 512) {
+    if (in_line) hipLaunchKernelGGL(moe_gate_up_kernel<true>, wide, block, 0, stream, p);
+    else hipLaunchKernelGGL(moe_gate_up_kernel<false>, wide, block, 0, stream, p);
+  } else {
+    if (in_line) hipLaunchKernelGGL(moe_gate_up_split_kernel<true>, narrow, block, 0, stream, p);
+    else hipLaunchKernelGGL(moe_gate_up_split_kernel<false>, narrow, block, 0, stream, p);
+  }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16), 1, chunks), dim3(1024), 0, stream, p);
