@@ -356,12 +356,12 @@ int nvfp4_moe_router(const void* x_bf16, const void* router_bf16, int64_t T, int
  *   H and I multiples of 32, at most 2^20; E in [1, 512]; top_k in [1, min(E, 16)]; T at most
  *   2^21 (else NVFP4_ERROR_INVALID_SHAPE). x, packed weights, out and workspace 16-byte
  *   aligned, scales, logits, topk_ids and topk_weights 4-byte aligned.
- *   The workspace holds at least nvfp4_mxfp4_moe_workspace_bytes(T, E, I, top_k) bytes. Calls
+ *   The workspace holds at least nvfp4_mxfp4_moe_workspace_bytes(T, E, H, I, top_k) bytes. Calls
  *   that may overlap in time need workspaces of their own. The result is deterministic for
  *   given arguments. Tokens are taken in groups of 64 that read their experts' weights each
  *   for itself: for long prompts, sort tokens by expert and use nvfp4_mxfp4_gemm.
  */
-size_t nvfp4_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k);
+size_t nvfp4_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k);
 int nvfp4_mxfp4_moe(const void* x_bf16, const void* logits, const void* w13_packed,
                     const void* w13_scales, const void* w2_packed, const void* w2_scales,
                     int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k, int renormalize,

@@ -54,7 +54,7 @@ SIGNATURES = {
     "nvfp4_mxfp4_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "nvfp4_mxfp4_linear": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, ctypes.c_size_t, _vp]),
     "nvfp4_moe_router": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp]),
-    "nvfp4_mxfp4_moe_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _i64]),
+    "nvfp4_mxfp4_moe_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _i64, _i64]),
     "nvfp4_mxfp4_moe": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int,
                                _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "nvfp4_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),

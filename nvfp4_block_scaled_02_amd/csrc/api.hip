@@ -161,16 +161,17 @@ bool moe_sizes(int64_t T, int64_t E, int64_t width) {
          width >= 32 && width % 32 == 0 && width <= ((int64_t)1 << 20);
 }
 struct MoeWorkspace {
-  size_t ids, weights, plan, h, bytes;  // offsets, and the whole
+  size_t ids, weights, plan, h, partial, bytes;  // offsets, and the whole
 };
-MoeWorkspace moe_workspace(int64_t T, int64_t E, int64_t I, int64_t top_k) {
+MoeWorkspace moe_workspace(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k) {
   const size_t slots = (size_t)(T * top_k);
   MoeWorkspace w;
   w.ids = 0;
   w.weights = w.ids + round_up(slots * 4, 256);
   w.plan = w.weights + round_up(slots * 4, 256);
   w.h = w.plan + round_up((size_t)nvfp4::moe_plan_bytes(T), 256);
-  w.bytes = w.h + round_up((size_t)nvfp4::moe_h_bytes(T, E, I, top_k), 256);
+  w.partial = w.h + round_up((size_t)nvfp4::moe_h_bytes(T, E, I, top_k), 256);
+  w.bytes = w.partial + round_up((size_t)nvfp4::moe_partial_bytes(T, H), 256);
   return w;
 }
 
@@ -470,9 +471,9 @@ int nvfp4_moe_router(const void* x, const void* w, int64_t T, int64_t E, int64_t
   return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
 }
 
-size_t nvfp4_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k) {
-  if (!moe_sizes(T, E, I) || top_k < 1 || top_k > E || top_k > nvfp4::kMoeMaxTopK) return 0;
-  const MoeWorkspace w = moe_workspace(T, E, I, top_k);
+size_t nvfp4_mxfp4_moe_workspace_bytes(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k) {
+  if (!moe_sizes(T, E, H) || !moe_sizes(T, E, I) || top_k < 1 || top_k > E || top_k > nvfp4::kMoeMaxTopK) return 0;
+  const MoeWorkspace w = moe_workspace(T, E, H, I, top_k);
   return w.bytes;
 }
 
@@ -490,7 +491,7 @@ int nvfp4_mxfp4_moe(const void* x, const void* logits, const void* w13p, const v
       !aligned(workspace, 16) || !aligned(logits, 4) || !aligned(w13s, 4) || !aligned(w2s, 4) ||
       !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
     return NVFP4_ERROR_MISALIGNED;
-  const MoeWorkspace w = moe_workspace(T, E, I, top_k);
+  const MoeWorkspace w = moe_workspace(T, E, H, I, top_k);
   if (workspace_bytes < w.bytes) return NVFP4_ERROR_WORKSPACE;
   if (T == 0) return NVFP4_SUCCESS;
   nvfp4::LaunchInfo info;
@@ -501,7 +502,7 @@ int nvfp4_mxfp4_moe(const void* x, const void* logits, const void* w13p, const v
                       (const uint8_t*)w13s, (const uint8_t*)w2p, (const uint8_t*)w2s,
                       (uint16_t*)out, topk_ids ? (int*)topk_ids : (int*)(base + w.ids),
                       topk_weights ? (float*)topk_weights : (float*)(base + w.weights),
-                      base + w.plan, base + w.h, T, H, I, (int)E, (int)top_k,
+                      base + w.plan, base + w.h, (float*)(base + w.partial), T, H, I, (int)E, (int)top_k,
                       renormalize == 1};
   hipError_t e = nvfp4::launch_moe(p, (hipStream_t)stream);
   return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);

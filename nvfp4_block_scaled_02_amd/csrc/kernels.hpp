@@ -160,6 +160,7 @@ struct MoeProblem {
   float* weights;           // [T, top_k]
   void* plan;               // moe_plan_bytes(T)
   uint8_t* h;               // moe_h_bytes(T, E, I, top_k): silu(gate) * up, bf16, in tiles
+  float* partial;           // moe_partial_bytes(T, H)
   int64_t T, H, I;
   int E, top_k;
   bool renormalize;
@@ -167,6 +168,7 @@ struct MoeProblem {
 constexpr int64_t kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxTokens = (int64_t)1 << 21;
 int64_t moe_plan_bytes(int64_t T);
 int64_t moe_h_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k);
+int64_t moe_partial_bytes(int64_t T, int64_t H);
 hipError_t launch_moe_router(const void* x, const void* w, int64_t T, int64_t E, int64_t H,
                              void* logits, hipStream_t stream);
 hipError_t launch_moe(const MoeProblem& p, hipStream_t stream);

@@ -681,6 +681,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
   __shared__ int s_first[kMoeExperts + 1];
   __shared__ int s_tile[kMoeExperts];
   __shared__ int s_slot[kMoeSlots];
+  __shared__ float s_weight[kMoeSlots];  // by slot (a load at its use would wait for all loads before it)
   const MoePlan* plan = (const MoePlan*)p.plan + blockIdx.z;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -697,12 +698,14 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
     s_tile[i] = plan->tile[i];
   }
   for (int i = threadIdx.x; i <= most; i += 64 * NW) s_first[i] = plan->first[i];
-  for (int i = threadIdx.x; i < n; i += 64 * NW) s_slot[i] = plan->slot[i];
+  for (int i = threadIdx.x; i < n; i += 64 * NW) {
+    s_slot[i] = plan->slot[i];
+    s_weight[i] = p.weights[t0 * p.top_k + i];
+  }
   for (int i = threadIdx.x; i < NW * nt * 4; i += 64 * NW)
     sums[i / (nt * 4)][i % (nt * 4) >> 2][i & 3] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
   uint8_t* h = h_tiles(p);
-  const float* weights = p.weights + t0 * p.top_k;
   const WeightLane lane_at(nb, lane);
   // pair (a, u): unit u of the a-th expert; a wave's next is NW units on
   struct Pair {
@@ -744,7 +747,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
       multiply_unit<1, 1>(acc, cur, lane, [&](int i, int) { return x.x[i]; });
       if (c0 + r < ns) {
         const int slot = s_slot[s0 + c0 + r];
-        sums[wave][slot / p.top_k][q] += weights[slot] * acc[0][0];
+        sums[wave][slot / p.top_k][q] += s_weight[slot] * acc[0][0];
       }
     }
   }
@@ -758,6 +761,160 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
   }
 }
 
+// The same for more tokens: 64 rows of W2 per workgroup, 16 per wave, so that a unit of h, staged
+// in LDS, serves four times the weights (with 16 rows the reads of h take the cache as long as
+// the weights take memory: 64 tokens 75 us). A workgroup takes one of `groups` shares of the
+// (expert, unit of K) pairs and writes its fp32 sums by token, which moe_combine_kernel adds.
+// Loads run two items ahead, into three buffers and three sets of registers: with one ahead a
+// unit's multiplications were all the time its successor's loads had (73 us against 57).
+constexpr int kSumPitch = 68;  // floats of a token's 64 sums: 16 columns in distinct banks
+
+__global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
+  constexpr int kBytes = kUnit * 1024;
+  __shared__ __align__(16) uint8_t lds[2 * kBytes];
+  __shared__ __align__(16) float sums[kMoeTokens * kSumPitch];
+  __shared__ int s_expert[kMoeExperts];
+  __shared__ int s_first[kMoeExperts + 1];
+  __shared__ int s_tile[kMoeExperts];
+  __shared__ int s_slot[kMoeSlots];
+  __shared__ float s_weight[kMoeSlots];  // by slot (a load at its use would wait for all loads before it)
+  const MoePlan* plan = (const MoePlan*)p.plan + blockIdx.z;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  // H % 32 == 0: a wave's 16 rows are all there or none (then it computes the first 16 again)
+  const bool mine = (int64_t)blockIdx.x * 64 + 16 * wave < p.H;
+  const int64_t o0 = mine ? (int64_t)blockIdx.x * 64 + 16 * wave : 0;
+  const int nb = (int)(p.I >> 5), nu = (nb + kUnit - 1) / kUnit;
+  const int64_t t0 = (int64_t)blockIdx.z * kMoeTokens;
+  const int nt = (int)min(p.T - t0, (int64_t)kMoeTokens);
+  const int n = nt * p.top_k, most = min(n, p.E);
+  const int active = plan->active;
+  for (int i = threadIdx.x; i < most; i += 256) {
+    s_expert[i] = plan->expert[i];
+    s_tile[i] = plan->tile[i];
+  }
+  for (int i = threadIdx.x; i <= most; i += 256) s_first[i] = plan->first[i];
+  for (int i = threadIdx.x; i < n; i += 256) {
+    s_slot[i] = plan->slot[i];
+    s_weight[i] = p.weights[t0 * p.top_k + i];
+  }
+  for (int i = threadIdx.x; i < nt * kSumPitch; i += 256) sums[i] = 0.0f;
+  __syncthreads();
+  const uint8_t* h = h_tiles(p);
+  const WeightLane lane_at(nb, lane);
+  // this group's pairs, [begin, end) in the order of (expert, unit)
+  const int64_t pairs = (int64_t)active * nu;
+  const int begin = (int)(pairs * blockIdx.y / gridDim.y), end = (int)(pairs * (blockIdx.y + 1) / gridDim.y);
+  // an item: unit u of expert a for the expert's tile c
+  struct Item {
+    int a, u, c;
+  };
+  const int a_end = end > 0 ? (end - 1) / nu : 0, a_begin = begin / nu;
+  auto u_first = [&](int a) { return a == a_begin ? begin - a * nu : 0; };
+  auto u_end = [&](int a) { return a == a_end ? end - a * nu : nu; };
+  auto slots_of = [&](int a) {
+    return __builtin_amdgcn_readfirstlane(s_first[a + 1]) - __builtin_amdgcn_readfirstlane(s_first[a]);
+  };
+  auto next = [&](Item k) {
+    if (++k.u < u_end(k.a)) return k;
+    if (16 * ++k.c >= slots_of(k.a)) {
+      ++k.a;
+      k.c = 0;
+    }
+    k.u = u_first(k.a);
+    return k;
+  };
+  // a lane's share of a unit of h: through registers, for a load that goes to LDS by itself would
+  // make every read of LDS wait for all loads in flight
+  struct HShare {
+    u32x4 v[kUnit / 4];
+  };
+  auto fetch = [&](HShare& s, const Item& k) {
+    const int ns = slots_of(k.a), b0 = unit_start(k.u, nb);
+    const int64_t tile = __builtin_amdgcn_readfirstlane(s_tile[k.a]) + k.c;
+    const __amdgpu_buffer_rsrc_t rh = make_rsrc(h + tile * (32 * p.I), (uint32_t)(32 * p.I));
+#pragma unroll
+    for (int j = 0; j < kUnit / 4; ++j) {
+      const int b = 4 * j + wave;  // 1 KiB: a block's four chunks of 16 columns
+      // columns that are not there and blocks that are not the unit's lie past the window: zeros
+      const uint32_t past = 16 * k.c + r < ns && unit_has(k.u, b0 + b, nb) ? 0u : 0x80000000u;
+      s.v[j] = __builtin_amdgcn_raw_buffer_load_b128(rh, (int)((16u * (uint32_t)lane) | past), (b0 + b) * 1024, 0);
+    }
+  };
+  auto stage = [&](const HShare& s, int buf) {
+#pragma unroll
+    for (int j = 0; j < kUnit / 4; ++j) *(u32x4*)&lds[buf * kBytes + (4 * j + wave) * 1024 + 16 * lane] = s.v[j];
+  };
+  auto load = [&](WeightUnit& w, const Item& k) {
+    const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(s_expert[k.a]) * p.H + o0;
+    load_unit(w, WeightRows{p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb}, lane_at, k.u, nb, lane);
+  };
+  if (begin < end) {
+    // turn i multiplies item i, puts h of item i + 1 into LDS and loads item i + 2 (past the last
+    // item the present one again), h before the weights, which are not waited for with it
+    Item at = {a_begin, begin - a_begin * nu, 0}, then = next(at);
+    auto there = [&](const Item& k) { return k.a <= a_end ? k : at; };
+    WeightUnit w0[1], w1[1], w2[1];
+    HShare hs;
+    fetch(hs, at);
+    load(w0[0], at);
+    stage(hs, 0);
+    fetch(hs, there(then));
+    load(w1[0], there(then));
+    floatx4 acc[1][1];
+    acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto turn = [&](WeightUnit (&now)[1], int buf, WeightUnit& fill) {
+      // item i's h is in LDS, and everyone is done with item i - 1's
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      const Item after = then.a <= a_end ? next(then) : then;
+      stage(hs, buf ^ 1);
+      fetch(hs, there(after));
+      load(fill, there(after));
+      __builtin_amdgcn_sched_barrier(0);
+      if (unit_cut(at.u, nb)) clear_unit(now[0], at.u, nb, lane);
+      multiply_unit<1, 1>(acc, now, lane, [&](int i, int) {
+        const int chunk = 16 * (i >> 2) + 4 * q + (i & 3);
+        return *(const u32x4*)&lds[buf * kBytes + (chunk * 16 + r) * 16];
+      });
+      if (at.u + 1 == u_end(at.a)) {
+        const int s0 = __builtin_amdgcn_readfirstlane(s_first[at.a]);
+        if (16 * at.c + r < slots_of(at.a)) {
+          const int slot = s_slot[s0 + 16 * at.c + r];
+          *(floatx4*)&sums[(slot / p.top_k) * kSumPitch + 16 * wave + 4 * q] += s_weight[slot] * acc[0][0];
+        }
+        acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      at = then;
+      then = after;
+      return at.a <= a_end;
+    };
+    while (turn(w0, 0, w2[0]) && turn(w1, 1, w0[0]) && turn(w2, 0, w1[0]) &&
+           turn(w0, 1, w2[0]) && turn(w1, 0, w0[0]) && turn(w2, 1, w1[0])) {
+    }
+  }
+  if (!mine) return;
+  // a wave's own columns
+  for (int i = lane; i < nt * 4; i += 64) {
+    const int t = i >> 2, o = i & 3;
+    const floatx4 v = *(const floatx4*)&sums[t * kSumPitch + 16 * wave + 4 * o];
+    *(floatx4*)&p.partial[(((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * min(p.T, (int64_t)kMoeTokens) + t) * p.H + o0 + 4 * o] = v;
+  }
+}
+
+// out = the sum of the groups' sums, in their order.
+__global__ void __launch_bounds__(256) moe_combine_kernel(MoeProblem p, int groups) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // of T * H / 4
+  if (i >= p.T * (p.H >> 2)) return;
+  const int64_t t = i / (p.H >> 2), o = (i - t * (p.H >> 2)) * 4, tokens = min(p.T, (int64_t)kMoeTokens);
+  const float* from = p.partial + (t / kMoeTokens * groups * tokens + t % kMoeTokens) * p.H + o;
+  floatx4 v = *(const floatx4*)from;
+  for (int g = 1; g < groups; ++g) v += *(const floatx4*)&from[(int64_t)g * tokens * p.H];
+  *(u32x2*)&p.out[t * p.H + o] = bf16x4_rne(v[0], v[1], v[2], v[3]);
+}
+
 }  // namespace
 
 int64_t moe_plan_bytes(int64_t T) {
@@ -767,6 +924,19 @@ int64_t moe_plan_bytes(int64_t T) {
 int64_t moe_h_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k) {
   const int64_t tokens = T < kMoeTokens ? T : kMoeTokens;
   return (T + kMoeTokens - 1) / kMoeTokens * moe_tiles(tokens * top_k, E) * (32 * I);
+}
+
+// Shares of the second product's pairs: two workgroups per compute unit, at most 8. 0: the
+// kernel without them, for few tokens.
+int moe_groups(int64_t T, int64_t H) {
+  if (T <= kInlineTokens) return 0;
+  const int64_t wide = (H + 63) / 64 * ((T + kMoeTokens - 1) / kMoeTokens), groups = 512 / wide;
+  return (int)(groups < 1 ? 1 : groups > 8 ? 8 : groups);
+}
+
+int64_t moe_partial_bytes(int64_t T, int64_t H) {
+  const int64_t tokens = T < kMoeTokens ? T : kMoeTokens;
+  return (T + kMoeTokens - 1) / kMoeTokens * tokens * moe_groups(T, H) * H * 4;
 }
 
 hipError_t launch_moe_router(const void* x, const void* w, int64_t T, int64_t E, int64_t H,
@@ -812,7 +982,15 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16), 1, chunks), dim3(1024), 0, stream, p);
+  const int groups = moe_groups(p.T, p.H);
+  if (groups == 0) {
+    hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16), 1, chunks), dim3(1024), 0, stream, p);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(moe_down_wide_kernel, dim3((unsigned)((p.H + 63) / 64), groups, chunks), dim3(256), 0, stream, p);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((p.T * (p.H / 4) + 255) / 256)), dim3(256), 0, stream, p, groups);
   return hipGetLastError();
 }
 

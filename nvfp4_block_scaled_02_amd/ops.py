@@ -375,8 +375,8 @@ def moe_router(x: torch.Tensor, router: torch.Tensor, logits: torch.Tensor | Non
     return logits
 
 
-def mxfp4_moe_workspace_bytes(T: int, E: int, I: int, top_k: int) -> int:
-    return int(load_library().nvfp4_mxfp4_moe_workspace_bytes(T, E, I, top_k))
+def mxfp4_moe_workspace_bytes(T: int, E: int, H: int, I: int, top_k: int) -> int:
+    return int(load_library().nvfp4_mxfp4_moe_workspace_bytes(T, E, H, I, top_k))
 
 
 def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
@@ -410,7 +410,7 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
         raise ValueError("expert weight or logit shapes are inconsistent")
     lib = _library()
     if workspace is None:
-        need = lib.nvfp4_mxfp4_moe_workspace_bytes(T, E, I, top_k)
+        need = lib.nvfp4_mxfp4_moe_workspace_bytes(T, E, H, I, top_k)
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
     _want(workspace, "workspace", torch.uint8, 1, dev)
     if out is None:

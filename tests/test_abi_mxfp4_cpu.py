@@ -90,11 +90,11 @@ def test_router(lib):
 
 def test_moe(lib):
     ws = lib.nvfp4_mxfp4_moe_workspace_bytes
-    assert ws(4, 8, 64, 2) > 4 * 2 * 64 * 2
-    for bad in ((-1, 8, 64, 2), (4, 0, 64, 1), (4, 513, 64, 2), (4, 8, 48, 2), (4, 8, 64, 0), (4, 8, 64, 9),
-                (4, 32, 64, 17)):
+    assert ws(4, 8, 64, 64, 2) > 4 * 2 * 64 * 2
+    for bad in ((-1, 8, 64, 64, 2), (4, 0, 64, 64, 1), (4, 513, 64, 64, 2), (4, 8, 64, 48, 2), (4, 8, 48, 64, 2),
+                (4, 8, 64, 64, 0), (4, 8, 64, 64, 9), (4, 32, 64, 64, 17)):
         assert ws(*bad) == 0, bad
-    base = [P, Q, P, Q, P, Q, 4, 8, 64, 64, 2, 1, P, Q, Q, P, ws(4, 8, 64, 2), NULL]
+    base = [P, Q, P, Q, P, Q, 4, 8, 64, 64, 2, 1, P, Q, Q, P, ws(4, 8, 64, 64, 2), NULL]
     call = _caller(lib.nvfp4_mxfp4_moe, base)
     for k in (0, 1, 2, 3, 4, 5, 12, 15):
         assert call({k: NULL}) == L.INVALID_VALUE
@@ -105,7 +105,7 @@ def test_moe(lib):
         assert call({k: ODD8}) == L.MISALIGNED
     for k in (1, 3, 5, 13, 14):
         assert call({k: ODD2}) == L.MISALIGNED
-    assert call({16: ws(4, 8, 64, 2) - 1}) == L.WORKSPACE
+    assert call({16: ws(4, 8, 64, 64, 2) - 1}) == L.WORKSPACE
     # no tokens: success without a device, routing outputs optional
     assert call({6: 0, 13: NULL, 14: NULL}) == L.SUCCESS
 

@@ -42,7 +42,7 @@ def _check(x, logits, w, dev, top_k, renormalize, label):
     E, I = w[0].shape[0], 2 * w[2].shape[2]
     say("moe", label, "T", T, "E", E, "k", top_k, "H", H, "I", I, renormalize)
     out, ok = guarded((T, H), torch.bfloat16)
-    work, ok_w = guarded((nv.mxfp4_moe_workspace_bytes(T, E, I, top_k),), torch.uint8, fill=0xFF)
+    work, ok_w = guarded((nv.mxfp4_moe_workspace_bytes(T, E, H, I, top_k),), torch.uint8, fill=0xFF)
     _, ids, weights = nv.mxfp4_moe(x, logits, *dev, top_k, renormalize=renormalize, out=out, workspace=work,
                                    return_routing=True)
     wid, wwt = M4.route(to_host(logits), top_k, renormalize)
@@ -173,7 +173,7 @@ def test_streams_and_graphs(T):
     x = xs[0].clone()
     logits = torch.empty((T, E), device="cuda")
     out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
-    work = torch.empty(nv.mxfp4_moe_workspace_bytes(T, E, I, k), dtype=torch.uint8, device="cuda")
+    work = torch.empty(nv.mxfp4_moe_workspace_bytes(T, E, H, I, k), dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
