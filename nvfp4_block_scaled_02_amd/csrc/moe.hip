@@ -60,8 +60,8 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const u32x4* __restrict
                                                          float* __restrict__ logits, int64_t T,
                                                          int64_t E, int64_t H8) {
   const int lane = threadIdx.x & 63;
-  const int64_t e0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kE;
-  const int64_t t0 = (int64_t)blockIdx.y * kT;
+  const int64_t e0 = ((int64_t)blockIdx.y * 4 + (threadIdx.x >> 6)) * kE;
+  const int64_t t0 = (int64_t)blockIdx.x * kT;
   if (e0 >= E) return;
   double acc[kE][kT] = {};
   for (int64_t i = lane; i < H8; i += 64) {
@@ -113,7 +113,7 @@ struct MoePlan {
 // h, between the two products, is kept in tiles of 16 slots of one expert, in the order in which
 // the second product's lanes take it: [tile][16-byte chunk of I][slot of the tile][16 bytes], so
 // that a load reads the slots' chunks side by side. (With a row per slot its loads, an access
-// for every lane, bounded that product: 64 tokens 81 us against 63.) Tiles that a chunk of
+// for every lane, bounded that product: 64 tokens 81 us against 75.) Tiles that a chunk of
 // tokens can need: one per expert reached and one more per 16 slots.
 __host__ __device__ inline int64_t moe_tiles(int64_t slots, int64_t E) {
   return (slots < E ? slots : E) + slots / 16;
@@ -432,8 +432,8 @@ __device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s
 
 // The same without a plan made before, for one to four tokens: every workgroup routes all of
 // them, a token per wave, and orders their at most 64 slots in a wave's lanes; the first one
-// writes the plan for the second product. (One token: a launch and its 5 us less, for 1 us in
-// each workgroup.) With at most 16 tokens an expert has one tile of h.
+// writes the plan for the second product. (One token: a launch and its 5 us less, for 3.5 us
+// in each workgroup.) With at most 16 tokens an expert has one tile of h.
 constexpr int kInlineTokens = 4;
 static_assert(kInlineTokens * kMoeTopK <= 64 && kInlineTokens <= kGateWaves, "a slot per lane, a token per wave");
 struct InlinePlan {
@@ -656,9 +656,12 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
     if (16 * t + r < s.n) *h_place(p, s, t, r, i0 + 4 * q) = gated(acc[0][t], acc[1][t]);
 }
 
-template <bool kInline>
-__global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProblem p) {
-  __shared__ __align__(16) uint8_t lds[kTiles * 16 * 1024];
+// An expert has at most as many slots as there are tokens: kMost = 1, for up to 16 tokens, takes
+// half the LDS and three workgroups per compute unit (12 tokens, 32 experts of
+// 2560 x 1440: the layer 62 -> 59 us).
+template <bool kInline, int kMost>
+__global__ void __launch_bounds__(64 * kGateWaves, kMost == 1 ? 3 : 2) moe_gate_up_kernel(MoeProblem p) {
+  __shared__ __align__(16) uint8_t lds[(kMost == 1 ? 2 : kMost) * 16 * 1024];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   ExpertSlots s;
@@ -666,9 +669,13 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_kernel(MoeProb
   const int64_t i0 = (int64_t)blockIdx.x * (16 * kGateWaves) + 16 * wave, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const bool mine = i0 < p.I;  // I % 32 == 0: a wave's 16 rows are all there or none
   const GateRows rows(p, s.expert, mine ? i0 : 0);
-  if (s.n <= 16) gate_up_tiles<1>(p, s, rows, mine, t0, i0, wave, lane, lds);
-  else if (s.n <= 32) gate_up_tiles<2>(p, s, rows, mine, t0, i0, wave, lane, lds);
-  else gate_up_tiles<4>(p, s, rows, mine, t0, i0, wave, lane, lds);
+  if constexpr (kMost == 1) {
+    gate_up_tiles<1>(p, s, rows, mine, t0, i0, wave, lane, lds);
+  } else {
+    if (s.n <= 16) gate_up_tiles<1>(p, s, rows, mine, t0, i0, wave, lane, lds);
+    else if (s.n <= 32) gate_up_tiles<2>(p, s, rows, mine, t0, i0, wave, lane, lds);
+    else gate_up_tiles<4>(p, s, rows, mine, t0, i0, wave, lane, lds);
+  }
 }
 
 // out[t, o] for 16 rows of W2 and one chunk of tokens: the workgroup's waves take (expert,
@@ -765,8 +772,8 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
 // in LDS, serves four times the weights (with 16 rows the reads of h take the cache as long as
 // the weights take memory: 64 tokens 75 us). A workgroup takes one of `groups` shares of the
 // (expert, unit of K) pairs and writes its fp32 sums by token, which moe_combine_kernel adds.
-// Loads run two items ahead, into three buffers and three sets of registers: with one ahead a
-// unit's multiplications were all the time its successor's loads had (73 us against 57).
+// Loads run two items ahead, into three sets of registers: with one ahead a
+// unit's multiplications were all the time its successor's loads had (64 tokens: 74 us against 67).
 constexpr int kSumPitch = 68;  // floats of a token's 64 sums: 16 columns in distinct banks
 
 __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
@@ -905,13 +912,19 @@ __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
 }
 
 // out = the sum of the groups' sums, in their order.
+constexpr int kMostGroups = 8;
 __global__ void __launch_bounds__(256) moe_combine_kernel(MoeProblem p, int groups) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // of T * H / 4
-  if (i >= p.T * (p.H >> 2)) return;
-  const int64_t t = i / (p.H >> 2), o = (i - t * (p.H >> 2)) * 4, tokens = min(p.T, (int64_t)kMoeTokens);
+  const int64_t o = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4, t = blockIdx.x;
+  if (o >= p.H) return;
+  const int64_t tokens = min(p.T, (int64_t)kMoeTokens);
   const float* from = p.partial + (t / kMoeTokens * groups * tokens + t % kMoeTokens) * p.H + o;
-  floatx4 v = *(const floatx4*)from;
-  for (int g = 1; g < groups; ++g) v += *(const floatx4*)&from[(int64_t)g * tokens * p.H];
+  floatx4 part[kMostGroups];  // all in flight at once
+#pragma unroll
+  for (int g = 0; g < kMostGroups; ++g) part[g] = *(const floatx4*)&from[(int64_t)min(g, groups - 1) * tokens * p.H];
+  floatx4 v = part[0];
+#pragma unroll
+  for (int g = 1; g < kMostGroups; ++g)
+    if (g < groups) v += part[g];
   *(u32x2*)&p.out[t * p.H + o] = bf16x4_rne(v[0], v[1], v[2], v[3]);
 }
 
@@ -927,11 +940,14 @@ int64_t moe_h_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k) {
 }
 
 // Shares of the second product's pairs: two workgroups per compute unit, at most 8. 0: the
-// kernel without them, for few tokens.
+// kernel without them, for few tokens. (Five layers of 16 to 256 experts, both sides in turn: at 5
+// and 8 tokens it is faster in five of ten, by 9%, and slower in four, by 7%; at 12 to 64 it is
+// slower in 18 of 25, by up to 18%.)
+constexpr int64_t kNarrowTokens = 8;
 int moe_groups(int64_t T, int64_t H) {
-  if (T <= kInlineTokens) return 0;
+  if (T <= kNarrowTokens) return 0;
   const int64_t wide = (H + 63) / 64 * ((T + kMoeTokens - 1) / kMoeTokens), groups = 512 / wide;
-  return (int)(groups < 1 ? 1 : groups > 8 ? 8 : groups);
+  return (int)(groups < 1 ? 1 : groups > kMostGroups ? kMostGroups : groups);
 }
 
 int64_t moe_partial_bytes(int64_t T, int64_t H) {
@@ -943,10 +959,10 @@ hipError_t launch_moe_router(const void* x, const void* w, int64_t T, int64_t E,
                              void* logits, hipStream_t stream) {
   // one or two tokens: an expert per wave, the most waves; more: blocks of 2 experts x 4 tokens
   if (T <= 2) {
-    hipLaunchKernelGGL((moe_router_kernel<1, 1>), dim3((unsigned)((E + 3) / 4), (unsigned)T), dim3(256), 0,
+    hipLaunchKernelGGL((moe_router_kernel<1, 1>), dim3((unsigned)T, (unsigned)((E + 3) / 4)), dim3(256), 0,
                        stream, (const u32x4*)x, (const u32x4*)w, (float*)logits, T, E, H / 8);
   } else {
-    hipLaunchKernelGGL((moe_router_kernel<2, 4>), dim3((unsigned)((E + 7) / 8), (unsigned)((T + 3) / 4)),
+    hipLaunchKernelGGL((moe_router_kernel<2, 4>), dim3((unsigned)((T + 3) / 4), (unsigned)((E + 7) / 8)),
                        dim3(256), 0, stream, (const u32x4*)x, (const u32x4*)w, (float*)logits, T, E, H / 8);
   }
   return hipGetLastError();
@@ -974,8 +990,9 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   const dim3 block(64 * kGateWaves);
   // workgroups of 64 rows where they are two per compute unit of an MI355X, else of 16
   if ((int64_t)wide.x * wide.y * wide.z >= 512) {
-    if (in_line) hipLaunchKernelGGL(moe_gate_up_kernel<true>, wide, block, 0, stream, p);
-    else hipLaunchKernelGGL(moe_gate_up_kernel<false>, wide, block, 0, stream, p);
+    if (in_line) hipLaunchKernelGGL((moe_gate_up_kernel<true, 1>), wide, block, 0, stream, p);
+    else if (p.T <= 16) hipLaunchKernelGGL((moe_gate_up_kernel<false, 1>), wide, block, 0, stream, p);
+    else hipLaunchKernelGGL((moe_gate_up_kernel<false, kTiles>), wide, block, 0, stream, p);
   } else {
     if (in_line) hipLaunchKernelGGL(moe_gate_up_split_kernel<true>, narrow, block, 0, stream, p);
     else hipLaunchKernelGGL(moe_gate_up_split_kernel<false>, narrow, block, 0, stream, p);
@@ -990,7 +1007,7 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   hipLaunchKernelGGL(moe_down_wide_kernel, dim3((unsigned)((p.H + 63) / 64), groups, chunks), dim3(256), 0, stream, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((p.T * (p.H / 4) + 255) / 256)), dim3(256), 0, stream, p, groups);
+  hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)p.T, (unsigned)((p.H + 1023) / 1024)), dim3(256), 0, stream, p, groups);
   return hipGetLastError();
 }
 

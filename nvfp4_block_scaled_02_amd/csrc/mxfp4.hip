@@ -729,6 +729,8 @@ constexpr Mx4Tile kMx4Tiles[] = {
     {NVFP4_MXFP4_TILE64, 64, 64, 2, 1.3f, 0.3f, 0.43f, 0.46f},
 };
 
+constexpr int64_t kMx4MaxTiles = (1 << 24) - 1;  // a launch has fewer than 2^32 threads
+
 }  // namespace
 
 // * Few rows: the kernel for them, while its staged scales fit its LDS and one or two passes
@@ -751,6 +753,7 @@ int plan_mx4_gemm(int64_t M, int64_t N, int64_t K, int64_t cus) {
   float least = 0.0f;
   for (const Mx4Tile& t : kMx4Tiles) {
     const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    if (best != 0 && tiles > kMx4MaxTiles) continue;  // (the largest tile comes first)
     const int64_t load = (tiles + cus - 1) / cus;  // tiles of the busiest compute unit
     const float base = t.base + (N % 8 != 0 ? t.ragged : 0.0f);
     float us;
@@ -770,7 +773,7 @@ int plan_mx4_gemm(int64_t M, int64_t N, int64_t K, int64_t cus) {
 
 hipError_t launch_mx4_gemm(const GemmProblem& p, hipStream_t stream, const LaunchInfo& dev) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
-  if (tiles(64, 64) > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (tiles(256, 256) > kMx4MaxTiles) return hipErrorInvalidValue;
 #define NVFP4_MX4_TILE(BM, BN, NBUF, KS)                                                              \
   hipLaunchKernelGGL((gemm_mx4_kernel<BM, BN, NBUF, KS>), dim3((unsigned)tiles(BM, BN)), dim3(256 * KS), 0, \
                      stream, p)

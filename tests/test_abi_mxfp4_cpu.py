@@ -64,6 +64,29 @@ def test_gemm(lib):
     assert call({4: 0}) == L.SUCCESS and call({5: 0}) == L.SUCCESS
 
 
+def test_gemm_plan(lib):
+    kind = ctypes.c_int(-1)
+    call = _caller(lib.nvfp4_mxfp4_gemm_plan, [8, 8, 64, 0, ctypes.byref(kind)])
+    assert call({4: None}) == L.INVALID_VALUE
+    for k in (0, 16, 40, 2**22 + 32):
+        assert call({2: k}) == L.INVALID_SHAPE
+    for v in (-1, 2**31):
+        assert call({0: v}) == L.INVALID_SHAPE and call({1: v}) == L.INVALID_SHAPE
+    assert call({}) == L.SUCCESS and kind.value == 0  # rows
+    assert nv.mxfp4_gemm_plan(8192, 8192, 8192) == "tile256"
+    assert nv.mxfp4_gemm_plan(8192, 8192, 8192, 256) == nv.mxfp4_gemm_plan(8192, 8192, 8192, -1)
+
+
+def test_gemm_plan_keeps_launches_below_two_to_the_32_threads(lib):
+    """The widths at which the tile of least estimated time would have too many workgroups."""
+    tiles = {"tile64": (64, 64), "tile64x128": (64, 128), "tile128": (128, 128), "tile128x256": (128, 256),
+             "tile256": (256, 256)}
+    top = 2**31 - 1
+    for m, n in ((1, top), (top, 1), (64, top), (top, 64), (65, 2**30 + 1), (2**30 + 1, 65), (1, 2**30), (300, 2**29)):
+        bm, bn = tiles[nv.mxfp4_gemm_plan(m, n, 32)]
+        assert -(-m // bm) * -(-n // bn) * 256 < 2**32, (m, n)
+
+
 def test_linear_and_its_workspace(lib):
     ws = lib.nvfp4_mxfp4_linear_workspace_bytes
     assert ws(8, 64) == 256 + 256 and ws(0, 64) == 0
