@@ -64,12 +64,16 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const u32x4* __restrict
   const int64_t t0 = (int64_t)blockIdx.x * kT;
   if (e0 >= E) return;
   double acc[kE][kT] = {};
+  u32x4 wv[kE], xv[kT], wn[kE], xn[kT];  // this turn's, and the next one's in flight
+  auto load = [&](u32x4 (&a)[kE], u32x4 (&b)[kT], int64_t i) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) a[e] = w[min(e0 + e, E - 1) * H8 + i];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) b[t] = x[min(t0 + t, T - 1) * H8 + i];
+  };
+  if (lane < H8) load(wv, xv, lane);
   for (int64_t i = lane; i < H8; i += 64) {
-    u32x4 wv[kE], xv[kT];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) wv[e] = w[min(e0 + e, E - 1) * H8 + i];
-#pragma unroll
-    for (int t = 0; t < kT; ++t) xv[t] = x[min(t0 + t, T - 1) * H8 + i];
+    load(wn, xn, min(i + 64, H8 - 1));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       auto element = [&](const u32x4& v) {
@@ -86,6 +90,10 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const u32x4* __restrict
         for (int e = 0; e < kE; ++e) acc[e][t] = __builtin_fma(xd, wd[e], acc[e][t]);
       }
     }
+#pragma unroll
+    for (int e = 0; e < kE; ++e) wv[e] = wn[e];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) xv[t] = xn[t];
   }
 #pragma unroll
   for (int e = 0; e < kE; ++e)
@@ -678,41 +686,36 @@ __global__ void __launch_bounds__(64 * kGateWaves, kMost == 1 ? 3 : 2) moe_gate_
   }
 }
 
-// out[t, o] for 16 rows of W2 and one chunk of tokens: the workgroup's waves take (expert,
-// unit of K) pairs in turn, a pair's weights and h in flight at once, and add the weighted
-// results to their own fp32 sums by token in LDS; the waves' sums are added in a fixed order.
+// out[t, o] for 16 rows of W2 and one to four tokens: the workgroup's waves take (expert, unit of
+// K) pairs in turn, a pair's weights and h in flight at once, and add the weighted results to
+// their own fp32 sums by token in LDS; the waves' sums are added in a fixed order. (One token,
+// 6 of 64 experts, 2048 x 1408: 6.5 us, of which the weights' 9.2 MB are 1.6.)
 __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
-  constexpr int NW = 16;
-  __shared__ floatx4 sums[NW][kMoeTokens][4];
-  __shared__ int s_expert[kMoeExperts];
-  __shared__ int s_first[kMoeExperts + 1];
-  __shared__ int s_tile[kMoeExperts];
-  __shared__ int s_slot[kMoeSlots];
-  __shared__ float s_weight[kMoeSlots];  // by slot (a load at its use would wait for all loads before it)
-  const MoePlan* plan = (const MoePlan*)p.plan + blockIdx.z;
+  constexpr int NW = 16, kSlots = kInlineTokens * kMoeTopK;
+  __shared__ floatx4 sums[NW][kInlineTokens][4];
+  __shared__ int s_expert[kSlots];
+  __shared__ int s_first[kSlots + 1];
+  __shared__ int s_slot[kSlots];
+  __shared__ float s_weight[kSlots];  // by slot (a load at its use would wait for all loads before it)
+  const MoePlan* plan = (const MoePlan*)p.plan;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15;
   const int64_t o0 = (int64_t)blockIdx.x * 16;
   const int nb = (int)(p.I >> 5), nu = (nb + kUnit - 1) / kUnit;
-  const int64_t t0 = (int64_t)blockIdx.z * kMoeTokens;
-  const int nt = (int)min(p.T - t0, (int64_t)kMoeTokens);
-  const int n = nt * p.top_k, most = min(n, p.E);
+  const int nt = (int)p.T, n = nt * p.top_k;
   const int active = plan->active;
   // the plan's lists, as long as they can be (past the active experts: of no meaning)
-  for (int i = threadIdx.x; i < most; i += 64 * NW) {
-    s_expert[i] = plan->expert[i];
-    s_tile[i] = plan->tile[i];
+  if (threadIdx.x < n) {
+    s_expert[threadIdx.x] = plan->expert[threadIdx.x];
+    s_slot[threadIdx.x] = plan->slot[threadIdx.x];
+    s_weight[threadIdx.x] = p.weights[threadIdx.x];
   }
-  for (int i = threadIdx.x; i <= most; i += 64 * NW) s_first[i] = plan->first[i];
-  for (int i = threadIdx.x; i < n; i += 64 * NW) {
-    s_slot[i] = plan->slot[i];
-    s_weight[i] = p.weights[t0 * p.top_k + i];
-  }
+  if (threadIdx.x <= n) s_first[threadIdx.x] = plan->first[threadIdx.x];
   for (int i = threadIdx.x; i < NW * nt * 4; i += 64 * NW)
     sums[i / (nt * 4)][i % (nt * 4) >> 2][i & 3] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
-  uint8_t* h = h_tiles(p);
+  const uint8_t* h = h_tiles(p);  // a tile for each expert
   const WeightLane lane_at(nb, lane);
   // pair (a, u): unit u of the a-th expert; a wave's next is NW units on
   struct Pair {
@@ -726,36 +729,26 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
     }
     return k;
   };
-  auto load = [&](WeightUnit& w, const Pair& k) {
-    const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(s_expert[k.a]) * p.H + o0;
-    load_unit(w, WeightRows{p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb}, lane_at, k.u, nb, lane);
-  };
-  WeightUnit cur[1];
+  WeightUnit w[1];
   ActUnit x = {};
-  Pair at = next(Pair{0, wave - NW});
-  while (at.a < active) {
+  for (Pair at = next(Pair{0, wave - NW}); at.a < active; at = next(at)) {
     const int s0 = __builtin_amdgcn_readfirstlane(s_first[at.a]);
     const int ns = __builtin_amdgcn_readfirstlane(s_first[at.a + 1]) - s0, u = at.u;
-    const uint8_t* tiles = h + (int64_t)__builtin_amdgcn_readfirstlane(s_tile[at.a]) * (32 * p.I);
-    auto load_tile = [&](int c0) {
-      load_acts<256>(x, make_rsrc(tiles + (int64_t)(c0 >> 4) * (32 * p.I), (uint32_t)(32 * p.I)), c0 + r < ns,
-                     16u * (uint32_t)r, u, nb, q);
-    };
-    load_tile(0);
-    load(cur[0], at);
-    at = next(at);
+    load_acts<256>(x, make_rsrc(h + (int64_t)at.a * (32 * p.I), (uint32_t)(32 * p.I)), r < ns, 16u * (uint32_t)r, u,
+                   nb, q);
+    const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(s_expert[at.a]) * p.H + o0;
+    load_unit(w[0], WeightRows{p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb}, lane_at, u, nb, lane);
     __builtin_amdgcn_sched_barrier(0);
-    if (unit_cut(u, nb)) clear_unit(cur[0], u, nb, lane);
-    for (int c0 = 0; c0 < ns; c0 += 16) {
-      if (c0 > 0) load_tile(c0);
-      if (unit_cut(u, nb)) clear_acts(x, u, nb, q);
-      floatx4 acc[1][1];
-      acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-      multiply_unit<1, 1>(acc, cur, lane, [&](int i, int) { return x.x[i]; });
-      if (c0 + r < ns) {
-        const int slot = s_slot[s0 + c0 + r];
-        sums[wave][slot / p.top_k][q] += s_weight[slot] * acc[0][0];
-      }
+    if (unit_cut(u, nb)) {
+      clear_unit(w[0], u, nb, lane);
+      clear_acts(x, u, nb, q);
+    }
+    floatx4 acc[1][1];
+    acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    multiply_unit<1, 1>(acc, w, lane, [&](int i, int) { return x.x[i]; });
+    if (r < ns) {
+      const int slot = s_slot[s0 + r];
+      sums[wave][slot / p.top_k][q] += s_weight[slot] * acc[0][0];
     }
   }
   __syncthreads();
@@ -763,17 +756,18 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
     const int t = i >> 2, o = i & 3;
     floatx4 v = sums[0][t][o];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) v += sums[w][t][o];
-    *(u32x2*)&p.out[(t0 + t) * p.H + o0 + 4 * o] = bf16x4_rne(v[0], v[1], v[2], v[3]);
+    for (int j = 1; j < NW; ++j) v += sums[j][t][o];
+    *(u32x2*)&p.out[t * p.H + o0 + 4 * o] = bf16x4_rne(v[0], v[1], v[2], v[3]);
   }
 }
 
 // The same for more tokens: 64 rows of W2 per workgroup, 16 per wave, so that a unit of h, staged
 // in LDS, serves four times the weights (with 16 rows the reads of h take the cache as long as
-// the weights take memory: 64 tokens 75 us). A workgroup takes one of `groups` shares of the
-// (expert, unit of K) pairs and writes its fp32 sums by token, which moe_combine_kernel adds.
-// Loads run two items ahead, into three sets of registers: with one ahead a
-// unit's multiplications were all the time its successor's loads had (64 tokens: 74 us against 67).
+// the weights take memory: 64 tokens, 8 of 128 experts, 4096 x 1024, 75 us). A workgroup takes
+// one of `groups` shares of the (expert, unit of K) pairs and writes its fp32 sums by token,
+// which moe_combine_kernel adds. Loads run two items ahead, into three sets of registers: with
+// one ahead a unit's multiplications were all the time its successor's loads had (74 us; now
+// 64, the weights at 4.5 TB/s, and 5 for the sums).
 constexpr int kSumPitch = 68;  // floats of a token's 64 sums: 16 columns in distinct banks
 
 __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
@@ -912,7 +906,7 @@ __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
 }
 
 // out = the sum of the groups' sums, in their order.
-constexpr int kMostGroups = 8;
+constexpr int kMostGroups = 16;
 __global__ void __launch_bounds__(256) moe_combine_kernel(MoeProblem p, int groups) {
   const int64_t o = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4, t = blockIdx.x;
   if (o >= p.H) return;
@@ -939,13 +933,13 @@ int64_t moe_h_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k) {
   return (T + kMoeTokens - 1) / kMoeTokens * moe_tiles(tokens * top_k, E) * (32 * I);
 }
 
-// Shares of the second product's pairs: two workgroups per compute unit, at most 8. 0: the
-// kernel without them, for few tokens. (Five layers of 16 to 256 experts, both sides in turn: at 5
-// and 8 tokens it is faster in five of ten, by 9%, and slower in four, by 7%; at 12 to 64 it is
-// slower in 18 of 25, by up to 18%.)
-constexpr int64_t kNarrowTokens = 8;
+// Shares of the second product's pairs: two workgroups per compute unit, at most kMostGroups (16
+// against 8: 64 tokens of 256 experts of 1024 x 512 in 73 us against 91; 32: another 3 less there,
+// 1 to 2 more elsewhere). 0: the kernel without shares, for up to four tokens (five layers of 16
+// to 256 experts, both sides in turn: at 2 and 4 tokens shares are slower in eight of ten, by up
+// to 5 us, at 5 and 8 faster in six, by up to 9).
 int moe_groups(int64_t T, int64_t H) {
-  if (T <= kNarrowTokens) return 0;
+  if (T <= kInlineTokens) return 0;
   const int64_t wide = (H + 63) / 64 * ((T + kMoeTokens - 1) / kMoeTokens), groups = 512 / wide;
   return (int)(groups < 1 ? 1 : groups > kMostGroups ? kMostGroups : groups);
 }
@@ -1001,7 +995,7 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const int groups = moe_groups(p.T, p.H);
   if (groups == 0) {
-    hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16), 1, chunks), dim3(1024), 0, stream, p);
+    hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16)), dim3(1024), 0, stream, p);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(moe_down_wide_kernel, dim3((unsigned)((p.H + 63) / 64), groups, chunks), dim3(256), 0, stream, p);

@@ -194,13 +194,22 @@ def mxfp8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Ten
 # the stream's handle is asked of PyTorch directly.
 
 
-def _want(t: torch.Tensor, name: str, dtype, ndim: int, index: int | None = None):
+def _first(t: torch.Tensor, name: str, dtype, ndim: int) -> int:
+    """_need, and the index of the tensor's device."""
+    index = t.get_device() if type(t) is torch.Tensor else -1
+    if index < 0 or t.dtype is not dtype or t.ndim != ndim or not t.is_contiguous():
+        _need(t, name, dtype, ndim)
+        return t.get_device()
+    return index
+
+
+def _want(t: torch.Tensor, name: str, dtype, ndim: int, index: int):
     """_need, and the tensor on device ``index``."""
-    if type(t) is not torch.Tensor or t.dtype is not dtype or t.ndim != ndim or not t.is_cuda \
+    if type(t) is not torch.Tensor or t.get_device() != index or t.dtype is not dtype or t.ndim != ndim \
             or not t.is_contiguous():
         _need(t, name, dtype, ndim)
-    if index is not None and t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{index}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{index}")
 
 
 def _library():
@@ -223,15 +232,14 @@ def _place(index: int, stream):
 
 def _elsewhere(index: int, stream) -> bool:
     """Whether a call has to change PyTorch's current device or stream."""
-    return stream is not None or index != torch.cuda.current_device()
+    return stream is not None or index != torch._C._cuda_getDevice()
 
 
 def mxfp4_quantize(x: torch.Tensor, packed: torch.Tensor | None = None,
                    scales: torch.Tensor | None = None, stream=None):
     """MXFP4 quantization: bf16 [M, K] -> packed E2M1 uint8 [M, K/2] + E8M0 scales
     [M, K/32]. A block with a NaN or an infinity becomes a NaN block (scale byte 0xFF)."""
-    _want(x, "x", torch.bfloat16, 2)
-    dev = x.get_device()
+    dev = _first(x, "x", torch.bfloat16, 2)
     if _elsewhere(dev, stream):
         with _place(dev, stream):
             return mxfp4_quantize(x, packed, scales)
@@ -239,11 +247,13 @@ def mxfp4_quantize(x: torch.Tensor, packed: torch.Tensor | None = None,
     if K % 32:
         raise ValueError("K must be a multiple of 32")
     if packed is None:
-        packed = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        packed = x.new_empty((M, K // 2), dtype=torch.uint8)
+    else:
+        _want(packed, "packed", torch.uint8, 2, dev)
     if scales is None:
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-    _want(packed, "packed", torch.uint8, 2, dev)
-    _want(scales, "scales", torch.uint8, 2, dev)
+        scales = x.new_empty((M, K // 32), dtype=torch.uint8)
+    else:
+        _want(scales, "scales", torch.uint8, 2, dev)
     if packed.shape != (M, K // 2) or scales.shape != (M, K // 32):
         raise ValueError("packed must be [M, K/2] and scales [M, K/32]")
     if M:
@@ -255,8 +265,7 @@ def mxfp4_quantize(x: torch.Tensor, packed: torch.Tensor | None = None,
 def mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None,
                      stream=None) -> torch.Tensor:
     """The values of an MXFP4 tensor as bf16 [M, K]."""
-    _want(packed, "packed", torch.uint8, 2)
-    dev = packed.get_device()
+    dev = _first(packed, "packed", torch.uint8, 2)
     _want(scales, "scales", torch.uint8, 2, dev)
     if _elsewhere(dev, stream):
         with _place(dev, stream):
@@ -265,10 +274,11 @@ def mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, out: torch.Tens
     if K % 32 or scales.shape != (M, K // 32):
         raise ValueError("packed must be [M, K/2] and scales [M, K/32], K a multiple of 32")
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=packed.device)
-    _want(out, "out", torch.bfloat16, 2, dev)
-    if out.shape != (M, K):
-        raise ValueError("out shape must be [M, K]")
+        out = packed.new_empty((M, K), dtype=torch.bfloat16)
+    else:
+        _want(out, "out", torch.bfloat16, 2, dev)
+        if out.shape != (M, K):
+            raise ValueError("out shape must be [M, K]")
     if M:
         check(_library().nvfp4_mxfp4_dequantize(packed.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(),
                                                 _raw_stream(dev)), "nvfp4_mxfp4_dequantize")
@@ -278,8 +288,7 @@ def mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, out: torch.Tens
 def mxfp4_gemm(a_packed: torch.Tensor, a_scales: torch.Tensor, w_packed: torch.Tensor,
                w_scales: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """MXFP4 GEMM: bf16 [M, N] = A_hat @ W_hat^T on the block-scaled fp4 MFMA."""
-    _want(a_packed, "a_packed", torch.uint8, 2)
-    dev = a_packed.get_device()
+    dev = _first(a_packed, "a_packed", torch.uint8, 2)
     _want(a_scales, "a_scales", torch.uint8, 2, dev)
     _want(w_packed, "w_packed", torch.uint8, 2, dev)
     _want(w_scales, "w_scales", torch.uint8, 2, dev)
@@ -292,10 +301,11 @@ def mxfp4_gemm(a_packed: torch.Tensor, a_scales: torch.Tensor, w_packed: torch.T
     if w_packed.shape != (N, Kh) or a_scales.shape != (M, K // 32) or w_scales.shape != (N, K // 32):
         raise ValueError("operand shapes are inconsistent")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a_packed.device)
-    _want(out, "out", torch.bfloat16, 2, dev)
-    if out.shape != (M, N):
-        raise ValueError("out shape must be [M, N]")
+        out = a_packed.new_empty((M, N), dtype=torch.bfloat16)
+    else:
+        _want(out, "out", torch.bfloat16, 2, dev)
+        if out.shape != (M, N):
+            raise ValueError("out shape must be [M, N]")
     if M and N:
         check(_library().nvfp4_mxfp4_gemm(a_packed.data_ptr(), a_scales.data_ptr(), w_packed.data_ptr(),
                                           w_scales.data_ptr(), M, N, K, out.data_ptr(), _raw_stream(dev)),
@@ -322,8 +332,7 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                  stream=None) -> torch.Tensor:
     """MXFP4 linear: quantize x, then the MXFP4 GEMM."""
-    _want(x, "x", torch.bfloat16, 2)
-    dev = x.get_device()
+    dev = _first(x, "x", torch.bfloat16, 2)
     _want(w_packed, "w_packed", torch.uint8, 2, dev)
     _want(w_scales, "w_scales", torch.uint8, 2, dev)
     if _elsewhere(dev, stream):
@@ -336,13 +345,15 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
     lib = _library()
     if workspace is None:
         need = lib.nvfp4_mxfp4_linear_workspace_bytes(M, K)
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
-    _want(workspace, "workspace", torch.uint8, 1, dev)
+        workspace = x.new_empty((max(need, 1),), dtype=torch.uint8)
+    else:
+        _want(workspace, "workspace", torch.uint8, 1, dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    _want(out, "out", torch.bfloat16, 2, dev)
-    if out.shape != (M, N):
-        raise ValueError("out shape must be [M, N]")
+        out = x.new_empty((M, N))
+    else:
+        _want(out, "out", torch.bfloat16, 2, dev)
+        if out.shape != (M, N):
+            raise ValueError("out shape must be [M, N]")
     if M and N:
         check(lib.nvfp4_mxfp4_linear(x.data_ptr(), w_packed.data_ptr(), w_scales.data_ptr(), M, N, K,
                                      out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)),
@@ -354,8 +365,7 @@ def moe_router(x: torch.Tensor, router: torch.Tensor, logits: torch.Tensor | Non
                stream=None) -> torch.Tensor:
     """Router logits of a mixture-of-experts layer: fp32 [T, E] = x @ router^T (x bf16 [T, H],
     router bf16 [E, H]), summed in fp64 and rounded once."""
-    _want(x, "x", torch.bfloat16, 2)
-    dev = x.get_device()
+    dev = _first(x, "x", torch.bfloat16, 2)
     _want(router, "router", torch.bfloat16, 2, dev)
     if _elsewhere(dev, stream):
         with _place(dev, stream):
@@ -365,10 +375,11 @@ def moe_router(x: torch.Tensor, router: torch.Tensor, logits: torch.Tensor | Non
     if router.shape[1] != H:
         raise ValueError("router must be [E, H]")
     if logits is None:
-        logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
-    _want(logits, "logits", torch.float32, 2, dev)
-    if logits.shape != (T, E):
-        raise ValueError("logits shape must be [T, E]")
+        logits = x.new_empty((T, E), dtype=torch.float32)
+    else:
+        _want(logits, "logits", torch.float32, 2, dev)
+        if logits.shape != (T, E):
+            raise ValueError("logits shape must be [T, E]")
     if T:
         check(_library().nvfp4_moe_router(x.data_ptr(), router.data_ptr(), T, E, H, logits.data_ptr(),
                                           _raw_stream(dev)), "nvfp4_moe_router")
@@ -391,8 +402,7 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
     ``renormalize``: the chosen experts' weights sum to one (else their share of the softmax
     over all experts). With ``return_routing`` the result is ``(out, ids int32 [T, top_k],
     weights fp32 [T, top_k])``. A row of logits that are all -inf has output 0."""
-    _want(x, "x", torch.bfloat16, 2)
-    dev = x.get_device()
+    dev = _first(x, "x", torch.bfloat16, 2)
     _want(logits, "logits", torch.float32, 2, dev)
     _want(w13_packed, "w13_packed", torch.uint8, 3, dev)
     _want(w13_scales, "w13_scales", torch.uint8, 3, dev)
@@ -411,18 +421,20 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
     lib = _library()
     if workspace is None:
         need = lib.nvfp4_mxfp4_moe_workspace_bytes(T, E, H, I, top_k)
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
-    _want(workspace, "workspace", torch.uint8, 1, dev)
+        workspace = x.new_empty((max(need, 1),), dtype=torch.uint8)
+    else:
+        _want(workspace, "workspace", torch.uint8, 1, dev)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    _want(out, "out", torch.bfloat16, 2, dev)
-    if out.shape != (T, H):
-        raise ValueError("out shape must be [T, H]")
+        out = x.new_empty((T, H))
+    else:
+        _want(out, "out", torch.bfloat16, 2, dev)
+        if out.shape != (T, H):
+            raise ValueError("out shape must be [T, H]")
     ids = weights = None
     if return_routing:
         n = max(int(top_k), 0)
-        ids = torch.empty((T, n), dtype=torch.int32, device=x.device)
-        weights = torch.empty((T, n), dtype=torch.float32, device=x.device)
+        ids = x.new_empty((T, n), dtype=torch.int32)
+        weights = x.new_empty((T, n), dtype=torch.float32)
     if T:
         check(lib.nvfp4_mxfp4_moe(x.data_ptr(), logits.data_ptr(), w13_packed.data_ptr(),
                                   w13_scales.data_ptr(), w2_packed.data_ptr(), w2_scales.data_ptr(), T, E, H,
