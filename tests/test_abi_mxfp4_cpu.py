@@ -133,6 +133,30 @@ def test_moe(lib):
     assert call({6: 0, 13: NULL, 14: NULL}) == L.SUCCESS
 
 
+def test_sizes_at_the_limits(lib):
+    """Sizes and statuses of extreme shapes against exact integers: an overflow would show."""
+    up = lambda v: -(-v // 256) * 256  # noqa: E731
+    values = [-(2**63), -1, 0, 1, 31, 32, 33, 64, 2**20, 2**20 + 32, 2**21, 2**21 + 1, 2**22, 2**22 + 32, 2**31 - 1,
+              2**31, 2**32, 2**40, 2**62, 2**63 - 1, 2**63 - 32]
+    kind = ctypes.c_int()
+    for M in values:
+        for K in values:
+            ok = 0 <= M < 2**31 and 32 <= K <= 2**22 and K % 32 == 0
+            assert lib.nvfp4_mxfp4_linear_workspace_bytes(M, K) == (up(M * K // 2) + up(M * K // 32) if ok else 0)
+            for N in (-1, 0, 1, 2**31 - 1, 2**31):
+                want = L.SUCCESS if ok and 0 <= N < 2**31 else L.INVALID_SHAPE
+                assert lib.nvfp4_mxfp4_gemm_plan(M, N, K, 256, ctypes.byref(kind)) == want, (M, N, K)
+    width = lambda v: 32 <= v <= 2**20 and v % 32 == 0  # noqa: E731
+    for T in values:
+        for E in (0, 1, 512, 513, 2**40):
+            for H in values[3:]:
+                for I in (32, 2**20, 2**20 + 32):
+                    got = lib.nvfp4_mxfp4_moe_workspace_bytes(T, E, H, I, 1)
+                    assert (got > 0) == (0 < T <= 2**21 and 1 <= E <= 512 and width(H) and width(I)), (T, E, H, I)
+                    if got:  # at least every chunk's h, and below what a sum past 2^63 would wrap to
+                        assert -(-T // 64) * 32 * I <= got < 2**62
+
+
 def test_no_device_is_reported(lib, gpu_available):
     if gpu_available:
         pytest.skip("a GPU is present")

@@ -117,6 +117,35 @@ def test_masked_and_unordered_logits():
             assert not to_host(out.float())[0].any()
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 7, 20])
+def test_masked_tokens_among_few(T):
+    """Masked, short, NaN and infinite rows where every workgroup routes for itself, and around it."""
+    E, k, H, I = 12, 3, 96, 64
+    inf, nan, low = float("inf"), float("nan"), torch.finfo(torch.float32).min
+    x, (w, dev) = _bf16((T, H), 4), _experts(E, H, I, 5)
+    rows = [(slice(None), -inf), (slice(1, None), -inf), (slice(None), low), (4, nan), (2, inf)]
+    for first in range(len(rows)):
+        l = torch.randn((T, E), device="cuda", generator=torch.Generator(device="cuda").manual_seed(first))
+        for t in range(min(T, 4)):
+            at, v = rows[(first + t) % len(rows)]
+            l[t, at] = v
+        for renormalize in (True, False):
+            out = to_host(_check(x, l, w, dev, k, renormalize, "masked").float())
+            for t in range(min(T, 4)):
+                if (first + t) % len(rows) == 0:
+                    assert not out[t].any()
+
+
+@pytest.mark.parametrize("T", [2, 4, 6])
+def test_nan_stays_with_its_token_among_few(T):
+    E, k, H, I = 6, 2, 160, 64
+    x, (w, dev) = _bf16((T, H), 1), _experts(E, H, I, 1)
+    l = torch.zeros((T, E), device="cuda")     # all to experts 0 and 1: one tile of columns
+    x[1, 150] = float("nan")
+    got = to_host(nv.mxfp4_moe(x, l, *dev, k).float())
+    assert np.isnan(got[1]).all() and not np.isnan(np.delete(got, 1, axis=0)).any()
+
+
 def test_every_token_masked():
     x, (w, dev) = _bf16((5, 64), 1), _experts(4, 64, 32, 1)
     l = torch.full((5, 4), -float("inf"), device="cuda")
