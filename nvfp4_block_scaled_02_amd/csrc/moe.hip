@@ -141,56 +141,62 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
 }
 __device__ __forceinline__ float key_logit(uint32_t k) { return u2f((k >> 31) ? k ^ 0x80000000u : ~k); }
 
-// The top_k of one token by one wave. Lane l holds experts l, l + 64, ...; each round takes
-// the largest key, the lowest index among equals. A row of fewer than top_k experts that
-// can be chosen ends in slots of id -1 and weight 0. Lane j < top_k returns the j-th choice.
+// The top_k of one token by one wave. Lane l holds experts l, l + 64, ... in kPer registers; each
+// round takes the largest key, the lowest index among equals. A row of fewer than top_k experts
+// that can be chosen ends in slots of id -1 and weight 0. Lane j < top_k returns the j-th choice.
 struct Choice {
   int id;
   float weight;
 };
-__device__ __forceinline__ Choice moe_topk(const float* __restrict__ row, int E, int top_k,
-                                           bool renormalize, int lane) {
-  constexpr int kPer = kMoeExperts / 64;
+template <int kPer>
+__device__ __forceinline__ Choice moe_topk_of(const float* __restrict__ row, int E, int top_k, bool renormalize,
+                                              int lane) {
   uint32_t key[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    key[i] = 0u;
-    if (64 * i < E && lane + 64 * i < E) key[i] = logit_key(row[lane + 64 * i]);
-  }
+  for (int i = 0; i < kPer; ++i) key[i] = lane + 64 * i < E ? logit_key(row[lane + 64 * i]) : 0u;
   Choice mine = {-1, 0.0f};
   float top = 0.0f, sum = 0.0f;
   for (int j = 0; j < top_k; ++j) {
-    uint32_t best = 0u;
-    int at = 0;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (64 * i < E && key[i] > best) {
-        best = key[i];
-        at = i;
-      }
+    for (int i = 1; i < kPer; ++i) best = max(best, key[i]);
     const uint32_t k = wave_max_u32(best);
     if (k == 0u) break;  // nothing left to choose
-    const uint32_t e = ~wave_max_u32(best == k ? ~(uint32_t)(lane + 64 * at) : 0u);
     if (j == 0) {
       top = key_logit(k);
       if (!renormalize) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          if (64 * i < E && key[i] != 0u) s += expf(key_logit(key[i]) - top);
+          if (key[i] != 0u) s += expf(key_logit(key[i]) - top);
         sum = wave_sum(s);
       }
     }
+    int e = -1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (64 * i < E && (uint32_t)(lane + 64 * i) == e) key[i] = 0u;
-    if (lane == j) mine = Choice{(int)e, key_logit(k)};
+      if (e < 0) {
+        const uint64_t at = __ballot(key[i] == k);
+        if (at != 0) {
+          const int first = __builtin_ctzll(at);
+          e = 64 * i + first;
+          if (lane == first) key[i] = 0u;
+        }
+      }
+    if (lane == j) mine = Choice{e, key_logit(k)};
   }
   // the choices' exponentials at once, in the lanes that hold them
   mine.weight = mine.id < 0 ? 0.0f : expf(mine.weight - top);
   if (renormalize) sum = wave_sum(mine.weight);
   if (mine.id >= 0) mine.weight /= sum;
   return mine;
+}
+__device__ __forceinline__ Choice moe_topk(const float* __restrict__ row, int E, int top_k, bool renormalize,
+                                           int lane) {
+  static_assert(kMoeExperts <= 512, "eight registers of 64 experts");
+  if (E <= 64) return moe_topk_of<1>(row, E, top_k, renormalize, lane);
+  if (E <= 128) return moe_topk_of<2>(row, E, top_k, renormalize, lane);
+  return moe_topk_of<8>(row, E, top_k, renormalize, lane);
 }
 __device__ __forceinline__ void route_token(const MoeProblem& p, int64_t t, int lane, int* chosen) {
   const Choice c = moe_topk(p.logits + t * p.E, p.E, p.top_k, p.renormalize, lane);

@@ -212,12 +212,22 @@ def _want(t: torch.Tensor, name: str, dtype, ndim: int, index: int):
             raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{index}")
 
 
+def _want_pair(packed: torch.Tensor, scales: torch.Tensor, prefix: str, ndim: int, index: int):
+    """_want of a packed tensor and its scales."""
+    if type(packed) is not torch.Tensor or type(scales) is not torch.Tensor or packed.get_device() != index \
+            or scales.get_device() != index or packed.dtype is not torch.uint8 or scales.dtype is not torch.uint8 \
+            or packed.ndim != ndim or scales.ndim != ndim or not packed.is_contiguous() \
+            or not scales.is_contiguous():
+        _want(packed, f"{prefix}packed", torch.uint8, ndim, index)
+        _want(scales, f"{prefix}scales", torch.uint8, ndim, index)
+
+
 def _library():
     return _lib._lib or load_library()
 
 
-def _raw_stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 @contextlib.contextmanager
@@ -230,17 +240,12 @@ def _place(index: int, stream):
         yield
 
 
-def _elsewhere(index: int, stream) -> bool:
-    """Whether a call has to change PyTorch's current device or stream."""
-    return stream is not None or index != torch._C._cuda_getDevice()
-
-
 def mxfp4_quantize(x: torch.Tensor, packed: torch.Tensor | None = None,
                    scales: torch.Tensor | None = None, stream=None):
     """MXFP4 quantization: bf16 [M, K] -> packed E2M1 uint8 [M, K/2] + E8M0 scales
     [M, K/32]. A block with a NaN or an infinity becomes a NaN block (scale byte 0xFF)."""
     dev = _first(x, "x", torch.bfloat16, 2)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev != _current_device():
         with _place(dev, stream):
             return mxfp4_quantize(x, packed, scales)
     M, K = x.shape
@@ -267,7 +272,7 @@ def mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, out: torch.Tens
     """The values of an MXFP4 tensor as bf16 [M, K]."""
     dev = _first(packed, "packed", torch.uint8, 2)
     _want(scales, "scales", torch.uint8, 2, dev)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev != _current_device():
         with _place(dev, stream):
             return mxfp4_dequantize(packed, scales, out)
     M, K = packed.shape[0], 2 * packed.shape[1]
@@ -290,15 +295,14 @@ def mxfp4_gemm(a_packed: torch.Tensor, a_scales: torch.Tensor, w_packed: torch.T
     """MXFP4 GEMM: bf16 [M, N] = A_hat @ W_hat^T on the block-scaled fp4 MFMA."""
     dev = _first(a_packed, "a_packed", torch.uint8, 2)
     _want(a_scales, "a_scales", torch.uint8, 2, dev)
-    _want(w_packed, "w_packed", torch.uint8, 2, dev)
-    _want(w_scales, "w_scales", torch.uint8, 2, dev)
-    if _elsewhere(dev, stream):
+    _want_pair(w_packed, w_scales, "w_", 2, dev)
+    if stream is not None or dev != _current_device():
         with _place(dev, stream):
             return mxfp4_gemm(a_packed, a_scales, w_packed, w_scales, out)
     M, Kh = a_packed.shape
-    N = w_packed.shape[0]
-    K = 2 * Kh
-    if w_packed.shape != (N, Kh) or a_scales.shape != (M, K // 32) or w_scales.shape != (N, K // 32):
+    N, Kw = w_packed.shape
+    K, Kb = 2 * Kh, Kh // 16
+    if Kw != Kh or a_scales.shape != (M, Kb) or w_scales.shape != (N, Kb):
         raise ValueError("operand shapes are inconsistent")
     if out is None:
         out = a_packed.new_empty((M, N), dtype=torch.bfloat16)
@@ -333,14 +337,13 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
                  stream=None) -> torch.Tensor:
     """MXFP4 linear: quantize x, then the MXFP4 GEMM."""
     dev = _first(x, "x", torch.bfloat16, 2)
-    _want(w_packed, "w_packed", torch.uint8, 2, dev)
-    _want(w_scales, "w_scales", torch.uint8, 2, dev)
-    if _elsewhere(dev, stream):
+    _want_pair(w_packed, w_scales, "w_", 2, dev)
+    if stream is not None or dev != _current_device():
         with _place(dev, stream):
             return mxfp4_linear(x, w_packed, w_scales, out, workspace)
     M, K = x.shape
-    N = w_packed.shape[0]
-    if w_packed.shape != (N, K // 2) or w_scales.shape != (N, K // 32):
+    N, Kw = w_packed.shape
+    if Kw != K // 2 or w_scales.shape != (N, K // 32):
         raise ValueError("weight shapes do not match x")
     lib = _library()
     if workspace is None:
@@ -367,12 +370,12 @@ def moe_router(x: torch.Tensor, router: torch.Tensor, logits: torch.Tensor | Non
     router bf16 [E, H]), summed in fp64 and rounded once."""
     dev = _first(x, "x", torch.bfloat16, 2)
     _want(router, "router", torch.bfloat16, 2, dev)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev != _current_device():
         with _place(dev, stream):
             return moe_router(x, router, logits)
     T, H = x.shape
-    E = router.shape[0]
-    if router.shape[1] != H:
+    E, Hr = router.shape
+    if Hr != H:
         raise ValueError("router must be [E, H]")
     if logits is None:
         logits = x.new_empty((T, E), dtype=torch.float32)
@@ -404,19 +407,17 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
     weights fp32 [T, top_k])``. A row of logits that are all -inf has output 0."""
     dev = _first(x, "x", torch.bfloat16, 2)
     _want(logits, "logits", torch.float32, 2, dev)
-    _want(w13_packed, "w13_packed", torch.uint8, 3, dev)
-    _want(w13_scales, "w13_scales", torch.uint8, 3, dev)
-    _want(w2_packed, "w2_packed", torch.uint8, 3, dev)
-    _want(w2_scales, "w2_scales", torch.uint8, 3, dev)
-    if _elsewhere(dev, stream):
+    _want_pair(w13_packed, w13_scales, "w13_", 3, dev)
+    _want_pair(w2_packed, w2_scales, "w2_", 3, dev)
+    if stream is not None or dev != _current_device():
         with _place(dev, stream):
             return mxfp4_moe(x, logits, w13_packed, w13_scales, w2_packed, w2_scales, top_k,
                              renormalize, out, workspace, return_routing)
     T, H = x.shape
-    E, I = w13_packed.shape[0], 2 * w2_packed.shape[2]
-    if logits.shape != (T, E) or w13_packed.shape != (E, 2 * I, H // 2) or \
-            w13_scales.shape != (E, 2 * I, H // 32) or w2_packed.shape != (E, H, I // 2) or \
-            w2_scales.shape != (E, H, I // 32):
+    E, I2, Hh = w13_packed.shape
+    I = I2 // 2
+    if logits.shape != (T, E) or Hh != H // 2 or I2 != 2 * I or w13_scales.shape != (E, I2, H // 32) or \
+            w2_packed.shape != (E, H, I // 2) or w2_scales.shape != (E, H, I // 32):
         raise ValueError("expert weight or logit shapes are inconsistent")
     lib = _library()
     if workspace is None:
