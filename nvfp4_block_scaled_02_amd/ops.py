@@ -426,7 +426,7 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
     else:
         _want(workspace, "workspace", torch.uint8, 1, dev)
     if out is None:
-        out = x.new_empty((T, H))
+        out = torch.empty_like(x)
     else:
         _want(out, "out", torch.bfloat16, 2, dev)
         if out.shape != (T, H):

@@ -1,5 +1,7 @@
 """The MXFP4 operators as a model's block runs them: a projection, the router, the routed experts,
 the residual sum and an output projection, eager and as one captured graph."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -86,3 +88,36 @@ def test_block(T):
         b(x)
         torch.cuda.synchronize()
         assert np.array_equal(got, to_host(b.y))
+
+
+def test_blocks_on_threads_at_once():
+    """Host threads, each with a stream and a block of its own, at once: the bits of a serial run."""
+    shapes = [(1, 16, 4, 512, 352, 1000), (4, 8, 2, 288, 96, 64), (17, 16, 4, 512, 352, 200), (70, 32, 8, 256, 64, 33)]
+    blocks = [Block(*s) for s in shapes]
+    xs = [_bf16((s[0], s[3]), 20 + i) for i, s in enumerate(shapes)]
+    want = []
+    for b, x in zip(blocks, xs):
+        b(x)
+        want.append(to_host(b.y).copy())
+    bad = []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(20):
+                    blocks[i].y.fill_(3.0)
+                    blocks[i](xs[i])
+            st.synchronize()
+            if not np.array_equal(blocks[i].y.view(torch.int16).cpu().numpy().view(np.uint16), want[i]):
+                bad.append(i)
+        except Exception as e:  # noqa: BLE001
+            bad.append((i, e))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(shapes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad

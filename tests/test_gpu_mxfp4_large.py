@@ -68,6 +68,33 @@ def test_moe(T):
     assert (np.abs(to_host(out.double()) - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("M", [2, 70])
+def test_gemm_at_the_longest_k(M):
+    K, N = 2**22, 5
+    say("mxfp4 gemm, longest K", M)
+    a, w = (_u8((M, K // 2), 1), _u8((M, K // 32), 2, 118, 131)), (_u8((N, K // 2), 3), _u8((N, K // 32), 4, 118, 131))
+    r = [0, M - 1]
+    ref, absref = M4.gemm_ref(_at(a[0], r), _at(a[1], r), to_host(w[0]), to_host(w[1]))
+    good, worst, nbad = O.check_gemm(to_host(nv.mxfp4_gemm(*a, *w))[r], ref, absref)
+    assert good, f"{nbad} out of tolerance (worst {worst:.3g})"
+
+
+@pytest.mark.parametrize("case", [(3, 2**20, 32), (6, 2**20, 32), (2, 32, 2**20), (6, 32, 2**20)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_moe_at_the_widest(case):
+    T, H, I = case
+    say("moe, widest", case)
+    sh, si = (109, 127) if H > I else (126, 109)   # scales that give sums of ordinary size
+    w = (_u8((1, 2 * I, H // 2), 1), _u8((1, 2 * I, H // 32), 2, sh, sh + 3),
+         _u8((1, H, I // 2), 3), _u8((1, H, I // 32), 4, si, si + 3))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn((T, H), device="cuda", generator=g).to(torch.bfloat16)
+    out = nv.mxfp4_moe(x, torch.zeros((T, 1), device="cuda"), *w, 1)
+    ref, tol = M4.moe_ref(to_host(x.double()), np.zeros((T, 1), dtype=np.int32), np.ones((T, 1)),
+                          M4.dequantize(*map(to_host, w[:2])), M4.dequantize(*map(to_host, w[2:])))
+    assert (np.abs(to_host(out.double()) - ref) <= tol).all()
+
+
 def test_router_of_many_tokens():
     T, E, H = 270001, 5, 32
     x = _u8((T, 2 * H), 1, 0, 0x40).view(torch.bfloat16)
