@@ -603,12 +603,13 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(M
 // (direct loads of one slot's 1 KiB per instruction). Chunk c (16 bytes) of row s sits at slot
 // c ^ (s % 16), so that the 16 columns of a fragment read are in distinct banks.
 // One barrier per unit: behind it the unit is readable, and the buffer of the unit before
-// takes the next. kT tiles of 16 slots; above 32 slots one buffer, filled between two barriers.
-template <int kT>
+// takes the next. kT tiles of 16 slots from slot c0 on; a single buffer is filled between two
+// barriers.
+template <int kT, int kBufs>
 __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertSlots& s, const GateRows& rows,
-                                              bool mine, int64_t t0, int64_t i0, int wave, int lane,
-                                              uint8_t* lds) {
-  constexpr int kBufs = kT <= 2 ? 2 : 1, kBytes = kT * 16 * 1024;
+                                              bool mine, int64_t t0, int64_t i0, int c0, int wave,
+                                              int lane, uint8_t* lds) {
+  constexpr int kBytes = kT * 16 * 1024;
   const int q = lane >> 4, r = lane & 15;
   const int nb = (int)(p.H >> 5), nu = (nb + kUnit - 1) / kUnit;
   const int64_t tokens = min(p.T - t0, (int64_t)kMoeTokens);
@@ -616,7 +617,7 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
   uint32_t row0[kT];  // where the activations of this lane's columns start
 #pragma unroll
   for (int t = 0; t < kT; ++t)
-    row0[t] = (uint32_t)(s.slots[min(16 * t + r, s.n - 1)] / p.top_k) * (uint32_t)(p.H * 2);
+    row0[t] = (uint32_t)(s.slots[min(c0 + 16 * t + r, s.n - 1)] / p.top_k) * (uint32_t)(p.H * 2);
   auto stage = [&](int u, int buf) {
     const uint32_t from = (uint32_t)unit_start(u, nb) * 64u;
 #pragma unroll
@@ -624,7 +625,7 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
 #pragma unroll
       for (int k = 0; k < 16 / kGateWaves; ++k) {
         const int row = kGateWaves * k + wave;  // of tile t
-        if (16 * t + row >= s.n) continue;
+        if (c0 + 16 * t + row >= s.n) continue;
         const int chunk = lane ^ row;
         // blocks that are not the unit's lie past the window: zeros
         const uint32_t past = unit_has(u, unit_start(u, nb) + (chunk >> 2), nb) ? 0u : 0x80000000u;
@@ -668,15 +669,18 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
   if (!mine) return;
 #pragma unroll
   for (int t = 0; t < kT; ++t)
-    if (16 * t + r < s.n) *h_place(p, s, t, r, i0 + 4 * q) = gated(acc[0][t], acc[1][t]);
+    if (c0 + 16 * t + r < s.n) *h_place(p, s, (c0 >> 4) + t, r, i0 + 4 * q) = gated(acc[0][t], acc[1][t]);
 }
 
-// An expert has at most as many slots as there are tokens: kMost = 1, for up to 16 tokens, takes
-// half the LDS and three workgroups per compute unit (12 tokens, 32 experts of
-// 2560 x 1440: the layer 62 -> 59 us).
-template <bool kInline, int kMost>
-__global__ void __launch_bounds__(64 * kGateWaves, kMost == 1 ? 3 : 2) moe_gate_up_kernel(MoeProblem p) {
-  __shared__ __align__(16) uint8_t lds[(kMost == 1 ? 2 : kMost) * 16 * 1024];
+// kFew: where experts have few slots, half the LDS and three workgroups per compute unit, for at
+// most 8 slots per expert on average, and up to 16 tokens (an expert has at most as many slots as
+// there are tokens). 64 tokens, two workgroups against three: 4 of 32 experts, 2560 x 1440, the
+// layer 68.5 us against 63.6; 6 of 64, 2048 x 1408, 85.6 against 82.8; 8 of 256, 1024 x 512, 72.7
+// against 69.5; 8 of 128, 4096 x 1024, 177 against 180; but 2 of 8, 4096 x 4096, 76 against 84: an
+// expert of more than 16 slots takes them 32 at a time, with registers that spill.
+template <bool kInline, bool kFew>
+__global__ void __launch_bounds__(64 * kGateWaves, kFew ? 3 : 2) moe_gate_up_kernel(MoeProblem p) {
+  __shared__ __align__(16) uint8_t lds[(kFew ? 2 : kTiles) * 16 * 1024];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   ExpertSlots s;
@@ -684,12 +688,17 @@ __global__ void __launch_bounds__(64 * kGateWaves, kMost == 1 ? 3 : 2) moe_gate_
   const int64_t i0 = (int64_t)blockIdx.x * (16 * kGateWaves) + 16 * wave, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const bool mine = i0 < p.I;  // I % 32 == 0: a wave's 16 rows are all there or none
   const GateRows rows(p, s.expert, mine ? i0 : 0);
-  if constexpr (kMost == 1) {
-    gate_up_tiles<1>(p, s, rows, mine, t0, i0, wave, lane, lds);
+  if (kInline || s.n <= 16) {
+    gate_up_tiles<1, 2>(p, s, rows, mine, t0, i0, 0, wave, lane, lds);
+  } else if constexpr (kFew) {
+    for (int c0 = 0; c0 < s.n; c0 += 32) {
+      if (c0 > 0) __syncthreads();
+      gate_up_tiles<2, 1>(p, s, rows, mine, t0, i0, c0, wave, lane, lds);
+    }
+  } else if (s.n <= 32) {
+    gate_up_tiles<2, 2>(p, s, rows, mine, t0, i0, 0, wave, lane, lds);
   } else {
-    if (s.n <= 16) gate_up_tiles<1>(p, s, rows, mine, t0, i0, wave, lane, lds);
-    else if (s.n <= 32) gate_up_tiles<2>(p, s, rows, mine, t0, i0, wave, lane, lds);
-    else gate_up_tiles<4>(p, s, rows, mine, t0, i0, wave, lane, lds);
+    gate_up_tiles<4, 1>(p, s, rows, mine, t0, i0, 0, wave, lane, lds);
   }
 }
 
@@ -993,9 +1002,9 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   const dim3 block(64 * kGateWaves);
   // workgroups of 64 rows where they are two per compute unit of an MI355X, else of 16
   if ((int64_t)wide.x * wide.y * wide.z >= 512) {
-    if (in_line) hipLaunchKernelGGL((moe_gate_up_kernel<true, 1>), wide, block, 0, stream, p);
-    else if (p.T <= 16) hipLaunchKernelGGL((moe_gate_up_kernel<false, 1>), wide, block, 0, stream, p);
-    else hipLaunchKernelGGL((moe_gate_up_kernel<false, kTiles>), wide, block, 0, stream, p);
+    if (in_line) hipLaunchKernelGGL((moe_gate_up_kernel<true, true>), wide, block, 0, stream, p);
+    else if (p.T <= 16 || slots <= 8 * (int64_t)p.E) hipLaunchKernelGGL((moe_gate_up_kernel<false, true>), wide, block, 0, stream, p);
+    else hipLaunchKernelGGL((moe_gate_up_kernel<false, false>), wide, block, 0, stream, p);
   } else {
     if (in_line) hipLaunchKernelGGL(moe_gate_up_split_kernel<true>, narrow, block, 0, stream, p);
     else hipLaunchKernelGGL(moe_gate_up_split_kernel<false>, narrow, block, 0, stream, p);

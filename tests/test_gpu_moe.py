@@ -117,6 +117,20 @@ def test_masked_and_unordered_logits():
             assert not to_host(out.float())[0].any()
 
 
+@pytest.mark.parametrize("crowd", [17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("experts", [32, 4])
+def test_crowded_experts(crowd, experts):
+    """`crowd` of 64 tokens at one expert, the others spread: experts far above the average number of slots, with
+    enough rows of weights for the workgroups that stage activations, and experts that all have many."""
+    T, k, H, I = 64, 2, 544, 32 * 64 * 17 // experts
+    say("crowded", crowd, experts)
+    x, (w, dev) = _bf16((T, H), 1), _experts(experts, H, I, 2)
+    l = torch.randn((T, experts), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    l[:crowd, experts // 2] = 9.0
+    l[crowd:, experts // 2] = -9.0
+    _check(x, l, w, dev, k, True, "crowded")
+
+
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 7, 20])
 def test_masked_tokens_among_few(T):
     """Masked, short, NaN and infinite rows where every workgroup routes for itself, and around it."""
