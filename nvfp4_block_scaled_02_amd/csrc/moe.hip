@@ -672,12 +672,14 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
     if (c0 + 16 * t + r < s.n) *h_place(p, s, (c0 >> 4) + t, r, i0 + 4 * q) = gated(acc[0][t], acc[1][t]);
 }
 
-// kFew: where experts have few slots, half the LDS and three workgroups per compute unit, for at
-// most 8 slots per expert on average, and up to 16 tokens (an expert has at most as many slots as
-// there are tokens). 64 tokens, two workgroups against three: 4 of 32 experts, 2560 x 1440, the
-// layer 68.5 us against 63.6; 6 of 64, 2048 x 1408, 85.6 against 82.8; 8 of 256, 1024 x 512, 72.7
-// against 69.5; 8 of 128, 4096 x 1024, 177 against 180; but 2 of 8, 4096 x 4096, 76 against 84: an
-// expert of more than 16 slots takes them 32 at a time, with registers that spill.
+// kFew: half the LDS and three workgroups per compute unit, so that more of them start at once.
+// For up to 16 tokens (an expert has at most as many slots as there are tokens; 24 layers and
+// numbers, two workgroups against three: 2% less on average, from 8% less to 8% more as the last
+// workgroups fall), and where a workgroup is short, below 8 units of K, and experts have at most 8
+// slots on average. 64 tokens: 4 of 32 experts, 2560 x 1440, the layer 68.5 us against 63.6; 8 of 256,
+// 1024 x 512, 72.7 against 69.5; but 8 of 128, 4096 x 1024, 175 against 179; 4 of 64, 4096 x 1024, 101
+// against 110; and 2 of 8, 4096 x 4096, 76 against 84: an expert of more than 16 slots takes them 32 at
+// a time, with registers that spill.
 template <bool kInline, bool kFew>
 __global__ void __launch_bounds__(64 * kGateWaves, kFew ? 3 : 2) moe_gate_up_kernel(MoeProblem p) {
   __shared__ __align__(16) uint8_t lds[(kFew ? 2 : kTiles) * 16 * 1024];
@@ -1003,7 +1005,8 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   // workgroups of 64 rows where they are two per compute unit of an MI355X, else of 16
   if ((int64_t)wide.x * wide.y * wide.z >= 512) {
     if (in_line) hipLaunchKernelGGL((moe_gate_up_kernel<true, true>), wide, block, 0, stream, p);
-    else if (p.T <= 16 || slots <= 8 * (int64_t)p.E) hipLaunchKernelGGL((moe_gate_up_kernel<false, true>), wide, block, 0, stream, p);
+    else if (p.T <= 16 || (p.H < 4096 && slots <= 8 * (int64_t)p.E))
+      hipLaunchKernelGGL((moe_gate_up_kernel<false, true>), wide, block, 0, stream, p);
     else hipLaunchKernelGGL((moe_gate_up_kernel<false, false>), wide, block, 0, stream, p);
   } else {
     if (in_line) hipLaunchKernelGGL(moe_gate_up_split_kernel<true>, narrow, block, 0, stream, p);
