@@ -1002,8 +1002,12 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   }
   const dim3 wide((unsigned)((p.I + 63) / 64), most, chunks), narrow((unsigned)(p.I / 16), most, chunks);
   const dim3 block(64 * kGateWaves);
-  // workgroups of 64 rows where they are two per compute unit of an MI355X, else of 16
-  if ((int64_t)wide.x * wide.y * wide.z >= 512) {
+  // Workgroups of 64 rows, whose waves take all units of K one after the other, where there is one
+  // for each of an MI355X's 256 compute units, with more than 8 units two; else of 16 rows with K over
+  // the waves. (The layer, 16 rows against 64: 4 tokens, 8 of 256 experts, 1024 x 512, 31 us
+  // against 24, 256 workgroups of 64 rows; 3 tokens, 6 of 64, 2048 x 1408, 38 against 34, 396; but
+  // 4 tokens, 2 of 16, 6144 x 2048, 39 against 50, 256; 1 token, 8 of 128, 4096 x 1024, 20 against 28, 128.)
+  if ((int64_t)wide.x * wide.y * wide.z >= (p.H <= 4096 ? 256 : 512)) {
     if (in_line) hipLaunchKernelGGL((moe_gate_up_kernel<true, true>), wide, block, 0, stream, p);
     else if (p.T <= 16 || (p.H < 4096 && slots <= 8 * (int64_t)p.E))
       hipLaunchKernelGGL((moe_gate_up_kernel<false, true>), wide, block, 0, stream, p);

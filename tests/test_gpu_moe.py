@@ -66,7 +66,8 @@ CASES = [  # T, E, top_k, H, I
     (1, 1, 1, 32, 32), (1, 4, 2, 64, 96), (1, 60, 6, 512, 352), (2, 8, 8, 96, 160), (3, 5, 2, 224, 64),
     (5, 16, 4, 1024, 480), (12, 32, 4, 640, 288), (16, 128, 8, 512, 128), (17, 7, 3, 160, 224), (31, 64, 8, 256, 256),
     (33, 4, 2, 288, 96), (64, 128, 8, 512, 192), (64, 2, 1, 128, 512), (65, 16, 4, 256, 160), (130, 8, 2, 192, 96),
-    (4, 512, 16, 128, 64), (64, 512, 16, 64, 32), (40, 8, 8, 2048, 64), (9, 16, 4, 64, 1440)]
+    (4, 512, 16, 128, 64), (64, 512, 16, 64, 32), (40, 8, 8, 2048, 64), (9, 16, 4, 64, 1440),
+    (3, 64, 6, 288, 1408), (4, 32, 8, 96, 544), (2, 40, 16, 4128, 544)]
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c)))
