@@ -346,8 +346,8 @@ int nvfp4_moe_router(const void* x_bf16, const void* router_bf16, int64_t T, int
  *     weight = softmax of the logits at the chosen expert, over all E (renormalize == 0) or
  *     over the chosen ones (renormalize == 1). A NaN logit ranks first; it, or a logit of
  *     +inf, makes that token's weights and output NaN.
- *   expert e: h = silu(Wg x) * (Wu x), rounded to bf16; y = W2 h. Gate rows Wg are rows
- *     0..I-1 of W13 [E, 2I, H], up rows Wu rows I..2I-1; W2 is [E, H, I].
+ *   expert e: h = silu(Wg x) * (Wu x), held to 2^-16 of its value; y = W2 h. Gate rows Wg are
+ *     rows 0..I-1 of W13 [E, 2I, H], up rows Wu rows I..2I-1; W2 is [E, H, I].
  *   out[t] = bf16_RNE(sum_j weight_tj y_tj), sums in fp32. Weights decode exactly; a value of
  *     2^128 or more reads as an infinity, a 0xFF scale byte as NaN.
  *   x_bf16 [T, H], logits fp32 [T, E]; w13_packed [E, 2I, H/2], w13_scales [E, 2I, H/32],

@@ -159,7 +159,7 @@ struct MoeProblem {
   int* ids;                 // [T, top_k]
   float* weights;           // [T, top_k]
   void* plan;               // moe_plan_bytes(T)
-  uint8_t* h;               // moe_h_bytes(T, E, I, top_k): silu(gate) * up, bf16, in tiles
+  uint8_t* h;               // moe_h_bytes(T, E, I, top_k): silu(gate) * up, two bf16 parts, in tiles
   float* partial;           // moe_partial_bytes(T, H)
   int64_t T, H, I;
   int E, top_k;

@@ -118,13 +118,18 @@ struct MoePlan {
   int slot[kMoeSlots];
 };
 
-// h, between the two products, is kept in tiles of 16 slots of one expert, in the order in which
-// the second product's lanes take it: [tile][16-byte chunk of I][slot of the tile][16 bytes], so
-// that a load reads the slots' chunks side by side. (With a row per slot its loads, an access
-// for every lane, bounded that product: 64 tokens 81 us against 75.) Tiles that a chunk of
-// tokens can need: one per expert reached and one more per 16 slots.
+// h, between the two products, is held in two bf16 parts that add up to it within 2^-16 of its
+// value, far below the rounding of the layer's output: the matrix instruction takes bf16, and h
+// rounded to it once was as much of the layer's error as the output's own rounding (relative to
+// 64 bits 2.3e-3 against 1.65e-3). The two parts are two columns of the instruction: a tile is
+// 8 slots of one expert, column 2n the n-th one's upper parts, 2n + 1 the lower, in the order in
+// which the second product's lanes take it, [tile][16-byte chunk of I][column][16 bytes], so that
+// a load reads the columns' chunks side by side. (With a row per slot its loads, an access for
+// every lane, bounded that product: 64 tokens 81 us against 75.) Tiles that a chunk of tokens can
+// need: one per expert reached and one more per 8 slots.
+constexpr int kTileSlots = 8;
 __host__ __device__ inline int64_t moe_tiles(int64_t slots, int64_t E) {
-  return (slots < E ? slots : E) + slots / 16;
+  return (slots < E ? slots : E) + slots / kTileSlots;
 }
 __device__ __forceinline__ uint8_t* h_tiles(const MoeProblem& p) {
   const int64_t tokens = min(p.T, (int64_t)kMoeTokens);
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
         const int o = __shfl_up(sum, off, 64);
         if (lane >= off) sum += o;
       }
-      const int ct = (c + 15) >> 4;
+      const int ct = (c + kTileSlots - 1) / kTileSlots;
       int tiles = ct;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -448,9 +453,10 @@ __device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s
 // The same without a plan made before, for one to four tokens: every workgroup routes all of
 // them, a token per wave, and orders their at most 64 slots in a wave's lanes; the first one
 // writes the plan for the second product. (One token: a launch and its 5 us less, for 2 us
-// in each workgroup.) With at most 16 tokens an expert has one tile of h.
+// in each workgroup.) With so few tokens an expert has one tile of h.
 constexpr int kInlineTokens = 4;
 static_assert(kInlineTokens * kMoeTopK <= 64 && kInlineTokens <= kGateWaves, "a slot per lane, a token per wave");
+static_assert(kInlineTokens <= kTileSlots, "a tile per expert");
 struct InlinePlan {
   int id[64];
   float weight[64];
@@ -532,18 +538,30 @@ struct GateRows {
   }
 };
 
-// Where tile t of an expert keeps its slot r's elements i .. i + 3 (i a multiple of 4).
-__device__ __forceinline__ u32x2* h_place(const MoeProblem& p, const ExpertSlots& s, int t, int r, int64_t i) {
-  return (u32x2*)(s.h + (int64_t)t * (32 * p.I) + ((i >> 3) * 16 + r) * 16 + 2 * (i & 7));
+// h = silu(g) * u of four rows, i .. i + 3 (i a multiple of 4), of an expert's n-th slot: the upper half
+// of its 32 bits (cut, so that it overflows with h alone) and the rest, rounded. An infinite h has
+// no rest; a NaN's may be anything.
+__device__ __forceinline__ void store_h(const MoeProblem& p, const ExpertSlots& s, int n, int64_t i,
+                                        const floatx4 g, const floatx4 u) {
+  uint32_t b[4];
+  float rest[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float v = g[j] / (1.0f + expf(-g[j])) * u[j];
+    b[j] = f2u(v);
+    rest[j] = (b[j] & 0x7FFFFFFFu) == 0x7F800000u ? 0.0f : v - u2f(b[j] & 0xFFFF0000u);
+  }
+  uint8_t* at = s.h + (int64_t)(n / kTileSlots) * (32 * p.I) + ((i >> 3) * 16 + 2 * (n % kTileSlots)) * 16 + 2 * (i & 7);
+  *(u32x2*)at = u32x2{(b[0] >> 16) | (b[1] & 0xFFFF0000u), (b[2] >> 16) | (b[3] & 0xFFFF0000u)};
+  *(u32x2*)(at + 16) = bf16x4_rne(rest[0], rest[1], rest[2], rest[3]);
 }
 
-// silu(g) * u of four rows, as bf16: h is rounded to the type of the activations that the next
-// product takes.
-__device__ __forceinline__ u32x2 gated(const floatx4 g, const floatx4 u) {
-  float v[4];
+// The products of a slot's two parts, added in both lanes (quad_perm [1, 0, 3, 2]).
+__device__ __forceinline__ floatx4 add_parts(floatx4 v) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
-  return bf16x4_rne(v[0], v[1], v[2], v[3]);
+  for (int j = 0; j < 4; ++j)
+    v[j] += u2f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f2u(v[j]), 0xB1, 0xF, 0xF, false));
+  return v;
 }
 
 // h[slot, i] = silu(gate) * up, few experts reached: 16 gate rows and their up rows per
@@ -593,7 +611,7 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(M
         g += part[w][0][lane];
         v += part[w][1][lane];
       }
-      *h_place(p, s, c0 >> 4, r, i0 + 4 * q) = gated(g, v);
+      store_h(p, s, c0 + r, i0 + 4 * q, g, v);
     }
   }
 }
@@ -669,7 +687,7 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
   if (!mine) return;
 #pragma unroll
   for (int t = 0; t < kT; ++t)
-    if (c0 + 16 * t + r < s.n) *h_place(p, s, (c0 >> 4) + t, r, i0 + 4 * q) = gated(acc[0][t], acc[1][t]);
+    if (c0 + 16 * t + r < s.n) store_h(p, s, c0 + 16 * t + r, i0 + 4 * q, acc[0][t], acc[1][t]);
 }
 
 // kFew: half the LDS and three workgroups per compute unit, so that more of them start at once.
@@ -752,8 +770,8 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
   for (Pair at = next(Pair{0, wave - NW}); at.a < active; at = next(at)) {
     const int s0 = __builtin_amdgcn_readfirstlane(s_first[at.a]);
     const int ns = __builtin_amdgcn_readfirstlane(s_first[at.a + 1]) - s0, u = at.u;
-    load_acts<256>(x, make_rsrc(h + (int64_t)at.a * (32 * p.I), (uint32_t)(32 * p.I)), r < ns, 16u * (uint32_t)r, u,
-                   nb, q);
+    load_acts<256>(x, make_rsrc(h + (int64_t)at.a * (32 * p.I), (uint32_t)(32 * p.I)), (r >> 1) < ns,
+                   16u * (uint32_t)r, u, nb, q);
     const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(s_expert[at.a]) * p.H + o0;
     load_unit(w[0], WeightRows{p.w2_packed + row * (p.I >> 1), p.w2_scales + row * nb}, lane_at, u, nb, lane);
     __builtin_amdgcn_sched_barrier(0);
@@ -764,9 +782,10 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
     floatx4 acc[1][1];
     acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     multiply_unit<1, 1>(acc, w, lane, [&](int i, int) { return x.x[i]; });
-    if (r < ns) {
-      const int slot = s_slot[s0 + r];
-      sums[wave][slot / p.top_k][q] += s_weight[slot] * acc[0][0];
+    const floatx4 y = add_parts(acc[0][0]);
+    if ((r & 1) == 0 && (r >> 1) < ns) {
+      const int slot = s_slot[s0 + (r >> 1)];
+      sums[wave][slot / p.top_k][q] += s_weight[slot] * y;
     }
   }
   __syncthreads();
@@ -790,7 +809,7 @@ constexpr int kSumPitch = 68;  // floats of a token's 64 sums: 16 columns in dis
 
 __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
   constexpr int kBytes = kUnit * 1024;
-  __shared__ __align__(16) uint8_t lds[2 * kBytes];
+  __shared__ __align__(16) uint8_t lds[3 * kBytes];  // a unit's first tiles in turn, its others
   __shared__ __align__(16) float sums[kMoeTokens * kSumPitch];
   __shared__ int s_expert[kMoeExperts];
   __shared__ int s_first[kMoeExperts + 1];
@@ -825,39 +844,35 @@ __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
   // this group's pairs, [begin, end) in the order of (expert, unit)
   const int64_t pairs = (int64_t)active * nu;
   const int begin = (int)(pairs * blockIdx.y / gridDim.y), end = (int)(pairs * (blockIdx.y + 1) / gridDim.y);
-  // an item: unit u of expert a for the expert's tile c
+  // an item: unit u of expert a, which has so many slots
   struct Item {
-    int a, u, c;
+    int a, u, slots;
   };
   const int a_end = end > 0 ? (end - 1) / nu : 0, a_begin = begin / nu;
-  auto u_first = [&](int a) { return a == a_begin ? begin - a * nu : 0; };
   auto u_end = [&](int a) { return a == a_end ? end - a * nu : nu; };
   auto slots_of = [&](int a) {
     return __builtin_amdgcn_readfirstlane(s_first[a + 1]) - __builtin_amdgcn_readfirstlane(s_first[a]);
   };
   auto next = [&](Item k) {
     if (++k.u < u_end(k.a)) return k;
-    if (16 * ++k.c >= slots_of(k.a)) {
-      ++k.a;
-      k.c = 0;
-    }
-    k.u = u_first(k.a);
+    k.u = 0;
+    if (++k.a <= a_end) k.slots = slots_of(k.a);
     return k;
   };
-  // a lane's share of a unit of h: through registers, for a load that goes to LDS by itself would
+  // a lane's share of a unit of h's tile c: through registers, for a load that goes to LDS by itself would
   // make every read of LDS wait for all loads in flight
   struct HShare {
     u32x4 v[kUnit / 4];
   };
-  auto fetch = [&](HShare& s, const Item& k) {
-    const int ns = slots_of(k.a), b0 = unit_start(k.u, nb);
-    const int64_t tile = __builtin_amdgcn_readfirstlane(s_tile[k.a]) + k.c;
+  auto fetch = [&](HShare& s, const Item& k, int c) {
+    const int b0 = unit_start(k.u, nb);
+    const int64_t tile = __builtin_amdgcn_readfirstlane(s_tile[k.a]) + c;
     const __amdgpu_buffer_rsrc_t rh = make_rsrc(h + tile * (32 * p.I), (uint32_t)(32 * p.I));
 #pragma unroll
     for (int j = 0; j < kUnit / 4; ++j) {
       const int b = 4 * j + wave;  // 1 KiB: a block's four chunks of 16 columns
       // columns that are not there and blocks that are not the unit's lie past the window: zeros
-      const uint32_t past = 16 * k.c + r < ns && unit_has(k.u, b0 + b, nb) ? 0u : 0x80000000u;
+      const uint32_t past = kTileSlots * c + (r >> 1) < k.slots && unit_has(k.u, b0 + b, nb) ? 0u : 0x80000000u;
       s.v[j] = __builtin_amdgcn_raw_buffer_load_b128(rh, (int)((16u * (uint32_t)lane) | past), (b0 + b) * 1024, 0);
     }
   };
@@ -871,40 +886,59 @@ __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
   };
   if (begin < end) {
     // turn i multiplies item i, puts h of item i + 1 into LDS and loads item i + 2 (past the last
-    // item the present one again), h before the weights, which are not waited for with it
-    Item at = {a_begin, begin - a_begin * nu, 0}, then = next(at);
+    // item the present one again), h before the weights, which are not waited for with it. Tiles of
+    // h past the item's first go through a buffer of their own against the same weights.
+    Item at = {a_begin, begin - a_begin * nu, slots_of(a_begin)}, then = next(at);
     auto there = [&](const Item& k) { return k.a <= a_end ? k : at; };
     WeightUnit w0[1], w1[1], w2[1];
-    HShare hs;
-    fetch(hs, at);
+    HShare hs, others;
+    fetch(hs, at, 0);
     load(w0[0], at);
     stage(hs, 0);
-    fetch(hs, there(then));
+    fetch(hs, there(then), 0);
     load(w1[0], there(then));
     floatx4 acc[1][1];
     acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto turn = [&](WeightUnit (&now)[1], int buf, WeightUnit& fill) {
-      // item i's h is in LDS, and everyone is done with item i - 1's
+    auto meet = [&]() {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-      const Item after = then.a <= a_end ? next(then) : then;
-      stage(hs, buf ^ 1);
-      fetch(hs, there(after));
-      load(fill, there(after));
-      __builtin_amdgcn_sched_barrier(0);
-      if (unit_cut(at.u, nb)) clear_unit(now[0], at.u, nb, lane);
+    };
+    auto multiply = [&](const WeightUnit (&now)[1], int buf) {
       multiply_unit<1, 1>(acc, now, lane, [&](int i, int) {
         const int chunk = 16 * (i >> 2) + 4 * q + (i & 3);
         return *(const u32x4*)&lds[buf * kBytes + (chunk * 16 + r) * 16];
       });
-      if (at.u + 1 == u_end(at.a)) {
-        const int s0 = __builtin_amdgcn_readfirstlane(s_first[at.a]);
-        if (16 * at.c + r < slots_of(at.a)) {
-          const int slot = s_slot[s0 + 16 * at.c + r];
-          *(floatx4*)&sums[(slot / p.top_k) * kSumPitch + 16 * wave + 4 * q] += s_weight[slot] * acc[0][0];
-        }
-        acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    auto add = [&](int c) {  // what acc holds of the item's tile c, to its tokens' sums
+      const int s0 = __builtin_amdgcn_readfirstlane(s_first[at.a]);
+      const floatx4 y = add_parts(acc[0][0]);
+      if ((r & 1) == 0 && kTileSlots * c + (r >> 1) < at.slots) {
+        const int slot = s_slot[s0 + kTileSlots * c + (r >> 1)];
+        *(floatx4*)&sums[(slot / p.top_k) * kSumPitch + 16 * wave + 4 * q] += s_weight[slot] * y;
+      }
+      acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    auto turn = [&](WeightUnit (&now)[1], int buf, WeightUnit& fill) {
+      meet();  // item i's h is in LDS, and everyone is done with item i - 1's
+      const Item after = then.a <= a_end ? next(then) : then;
+      const int tiles = (at.slots + kTileSlots - 1) / kTileSlots;
+      stage(hs, buf ^ 1);
+      if (tiles > 1) fetch(others, at, 1);
+      fetch(hs, there(after), 0);
+      load(fill, there(after));
+      __builtin_amdgcn_sched_barrier(0);
+      if (unit_cut(at.u, nb)) clear_unit(now[0], at.u, nb, lane);
+      multiply(now, buf);
+      // an only tile's units add up in registers
+      if (tiles > 1 || at.u + 1 == u_end(at.a)) add(0);
+      for (int c = 1; c < tiles; ++c) {
+        if (c > 1) meet();
+        stage(others, 2);
+        meet();
+        if (c + 1 < tiles) fetch(others, at, c + 1);
+        multiply(now, 2);
+        add(c);
       }
       at = then;
       then = after;

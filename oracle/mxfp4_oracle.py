@@ -81,14 +81,15 @@ def route(logits: np.ndarray, top_k: int, renormalize: bool):
     return ids, weights
 
 
-def moe_ref(x, ids, weights, w13, w2):
+def moe_ref(x, ids, weights, w13, w2, h_error=2.0**-8):
     """(out, tol) [T, H] of activations x [T, H] under a routing, with decoded weights w13
     [E, 2I, H] and w2 [E, H, I], all float64.
 
     ``tol`` bounds a correct result's error, to first order: a sum of n products in fp32 is
     off by at most n 2^-24 of its terms' magnitudes (any order), |silu'| <= 1.1 and
-    |silu(g)| <= |g|; h is rounded to bf16 once (2^-8 of its value) after an exponential and
-    a division good to 2^-20; routing weights are good to 2^-20; out is rounded to bf16."""
+    |silu(g)| <= |g|; h is held to ``h_error`` of its value (2^-8: rounded to bf16 once) after an
+    exponential and a division good to 2^-20; routing weights are good to 2^-20; out is rounded
+    to bf16."""
     T, H = x.shape
     I = w2.shape[2]
     out, tol = np.zeros((T, H)), np.zeros((T, H))
@@ -103,6 +104,6 @@ def moe_ref(x, ids, weights, w13, w2):
                 h = g / (1.0 + np.exp(-g)) * u
             out[t] += weights[t, j] * (w2[e] @ h)
             sg, su = np.abs(w13[e, :I]) @ np.abs(x[t]), np.abs(w13[e, I:]) @ np.abs(x[t])
-            dh = 1.1 * eh * sg * np.abs(u) + eh * np.abs(g) * su + (2.0**-8 + 2.0**-19) * np.abs(h)
+            dh = 1.1 * eh * sg * np.abs(u) + eh * np.abs(g) * su + (h_error + 2.0**-19) * np.abs(h)
             tol[t] += np.abs(weights[t, j]) * (np.abs(w2[e]) @ (dh + (ei + 2.0**-19) * np.abs(h)))
     return out, tol + 2.0**-8 * (np.abs(out) + tol)
