@@ -226,8 +226,9 @@ def _library():
     return _lib._lib or load_library()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (a PyTorch built without a GPU has neither, and no tensor that gets as far as their use)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 @contextlib.contextmanager
