@@ -196,7 +196,7 @@ def mxfp8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Ten
 
 def _first(t: torch.Tensor, name: str, dtype, ndim: int) -> int:
     """_need, and the index of the tensor's device."""
-    index = t.get_device() if type(t) is torch.Tensor else -1
+    index = t.get_device() if isinstance(t, torch.Tensor) else -1
     if index < 0 or t.dtype is not dtype or t.ndim != ndim or not t.is_contiguous():
         _need(t, name, dtype, ndim)
         return t.get_device()
@@ -205,7 +205,7 @@ def _first(t: torch.Tensor, name: str, dtype, ndim: int) -> int:
 
 def _want(t: torch.Tensor, name: str, dtype, ndim: int, index: int):
     """_need, and the tensor on device ``index``."""
-    if type(t) is not torch.Tensor or t.get_device() != index or t.dtype is not dtype or t.ndim != ndim \
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype is not dtype or t.ndim != ndim \
             or not t.is_contiguous():
         _need(t, name, dtype, ndim)
         if t.get_device() != index:
@@ -214,8 +214,9 @@ def _want(t: torch.Tensor, name: str, dtype, ndim: int, index: int):
 
 def _want_pair(packed: torch.Tensor, scales: torch.Tensor, prefix: str, ndim: int, index: int):
     """_want of a packed tensor and its scales."""
-    if type(packed) is not torch.Tensor or type(scales) is not torch.Tensor or packed.get_device() != index \
-            or scales.get_device() != index or packed.dtype is not torch.uint8 or scales.dtype is not torch.uint8 \
+    if not isinstance(packed, torch.Tensor) or not isinstance(scales, torch.Tensor) \
+            or packed.get_device() != index or scales.get_device() != index \
+            or packed.dtype is not torch.uint8 or scales.dtype is not torch.uint8 \
             or packed.ndim != ndim or scales.ndim != ndim or not packed.is_contiguous() \
             or not scales.is_contiguous():
         _want(packed, f"{prefix}packed", torch.uint8, ndim, index)
