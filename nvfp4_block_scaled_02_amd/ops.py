@@ -191,7 +191,10 @@ def mxfp8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Ten
 # The calls below are made once per layer for a single token, where the host's part of a call
 # is as long as the kernel: their checks are one expression per tensor that falls back to _need
 # (and its messages) only when something is wrong, pointers go to the library as integers, and
-# the stream's handle is asked of PyTorch directly.
+# the stream's handle is asked of PyTorch directly. Empty calls go to the library as well, which
+# checks them like any other: PyTorch has no address for an empty tensor, and any that is not
+# null and aligned will do.
+_EMPTY = 256
 
 
 def _first(t: torch.Tensor, name: str, dtype, ndim: int) -> int:
@@ -263,9 +266,8 @@ def mxfp4_quantize(x: torch.Tensor, packed: torch.Tensor | None = None,
         _want(scales, "scales", torch.uint8, 2, dev)
     if packed.shape != (M, K // 2) or scales.shape != (M, K // 32):
         raise ValueError("packed must be [M, K/2] and scales [M, K/32]")
-    if M:
-        check(_library().nvfp4_mxfp4_quantize(x.data_ptr(), M, K, packed.data_ptr(), scales.data_ptr(),
-                                              _raw_stream(dev)), "nvfp4_mxfp4_quantize")
+    check(_library().nvfp4_mxfp4_quantize(x.data_ptr() or _EMPTY, M, K, packed.data_ptr() or _EMPTY,
+                                          scales.data_ptr() or _EMPTY, _raw_stream(dev)), "nvfp4_mxfp4_quantize")
     return packed, scales
 
 
@@ -286,9 +288,8 @@ def mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, out: torch.Tens
         _want(out, "out", torch.bfloat16, 2, dev)
         if out.shape != (M, K):
             raise ValueError("out shape must be [M, K]")
-    if M:
-        check(_library().nvfp4_mxfp4_dequantize(packed.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(),
-                                                _raw_stream(dev)), "nvfp4_mxfp4_dequantize")
+    check(_library().nvfp4_mxfp4_dequantize(packed.data_ptr() or _EMPTY, scales.data_ptr() or _EMPTY, M, K,
+                                            out.data_ptr() or _EMPTY, _raw_stream(dev)), "nvfp4_mxfp4_dequantize")
     return out
 
 
@@ -312,10 +313,9 @@ def mxfp4_gemm(a_packed: torch.Tensor, a_scales: torch.Tensor, w_packed: torch.T
         _want(out, "out", torch.bfloat16, 2, dev)
         if out.shape != (M, N):
             raise ValueError("out shape must be [M, N]")
-    if M and N:
-        check(_library().nvfp4_mxfp4_gemm(a_packed.data_ptr(), a_scales.data_ptr(), w_packed.data_ptr(),
-                                          w_scales.data_ptr(), M, N, K, out.data_ptr(), _raw_stream(dev)),
-              "nvfp4_mxfp4_gemm")
+    check(_library().nvfp4_mxfp4_gemm(a_packed.data_ptr() or _EMPTY, a_scales.data_ptr() or _EMPTY,
+                                      w_packed.data_ptr() or _EMPTY, w_scales.data_ptr() or _EMPTY, M, N, K,
+                                      out.data_ptr() or _EMPTY, _raw_stream(dev)), "nvfp4_mxfp4_gemm")
     return out
 
 
@@ -359,10 +359,10 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
         _want(out, "out", torch.bfloat16, 2, dev)
         if out.shape != (M, N):
             raise ValueError("out shape must be [M, N]")
-    if M and N:
-        check(lib.nvfp4_mxfp4_linear(x.data_ptr(), w_packed.data_ptr(), w_scales.data_ptr(), M, N, K,
-                                     out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)),
-              "nvfp4_mxfp4_linear")
+    check(lib.nvfp4_mxfp4_linear(x.data_ptr() or _EMPTY, w_packed.data_ptr() or _EMPTY,
+                                 w_scales.data_ptr() or _EMPTY, M, N, K, out.data_ptr() or _EMPTY,
+                                 workspace.data_ptr() or _EMPTY, workspace.numel(), _raw_stream(dev)),
+          "nvfp4_mxfp4_linear")
     return out
 
 
@@ -385,9 +385,8 @@ def moe_router(x: torch.Tensor, router: torch.Tensor, logits: torch.Tensor | Non
         _want(logits, "logits", torch.float32, 2, dev)
         if logits.shape != (T, E):
             raise ValueError("logits shape must be [T, E]")
-    if T:
-        check(_library().nvfp4_moe_router(x.data_ptr(), router.data_ptr(), T, E, H, logits.data_ptr(),
-                                          _raw_stream(dev)), "nvfp4_moe_router")
+    check(_library().nvfp4_moe_router(x.data_ptr() or _EMPTY, router.data_ptr() or _EMPTY, T, E, H,
+                                      logits.data_ptr() or _EMPTY, _raw_stream(dev)), "nvfp4_moe_router")
     return logits
 
 
@@ -438,13 +437,12 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
         n = max(int(top_k), 0)
         ids = x.new_empty((T, n), dtype=torch.int32)
         weights = x.new_empty((T, n), dtype=torch.float32)
-    if T:
-        check(lib.nvfp4_mxfp4_moe(x.data_ptr(), logits.data_ptr(), w13_packed.data_ptr(),
-                                  w13_scales.data_ptr(), w2_packed.data_ptr(), w2_scales.data_ptr(), T, E, H,
-                                  I, top_k, int(bool(renormalize)), out.data_ptr(),
-                                  ids.data_ptr() if return_routing else None,
-                                  weights.data_ptr() if return_routing else None, workspace.data_ptr(),
-                                  workspace.numel(), _raw_stream(dev)), "nvfp4_mxfp4_moe")
+    check(lib.nvfp4_mxfp4_moe(x.data_ptr() or _EMPTY, logits.data_ptr() or _EMPTY, w13_packed.data_ptr() or _EMPTY,
+                              w13_scales.data_ptr() or _EMPTY, w2_packed.data_ptr() or _EMPTY,
+                              w2_scales.data_ptr() or _EMPTY, T, E, H, I, top_k, int(bool(renormalize)),
+                              out.data_ptr() or _EMPTY, ids.data_ptr() if return_routing else None,
+                              weights.data_ptr() if return_routing else None, workspace.data_ptr() or _EMPTY,
+                              workspace.numel(), _raw_stream(dev)), "nvfp4_mxfp4_moe")
     return (out, ids, weights) if return_routing else out
 
 
