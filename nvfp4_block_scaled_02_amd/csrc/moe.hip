@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "gemm_common.hpp"
+#include "moe_offsets.hpp"
 
 namespace nvfp4 {
 
@@ -125,12 +126,7 @@ struct MoePlan {
 // 8 slots of one expert, column 2n the n-th one's upper parts, 2n + 1 the lower, in the order in
 // which the second product's lanes take it, [tile][16-byte chunk of I][column][16 bytes], so that
 // a load reads the columns' chunks side by side. (With a row per slot its loads, an access for
-// every lane, bounded that product: 64 tokens 81 us against 75.) Tiles that a chunk of tokens can
-// need: one per expert reached and one more per 8 slots.
-constexpr int kTileSlots = 8;
-__host__ __device__ inline int64_t moe_tiles(int64_t slots, int64_t E) {
-  return (slots < E ? slots : E) + slots / kTileSlots;
-}
+// every lane, bounded that product: 64 tokens 81 us against 75.)
 __device__ __forceinline__ uint8_t* h_tiles(const MoeProblem& p) {
   const int64_t tokens = min(p.T, (int64_t)kMoeTokens);
   return (uint8_t*)p.h + (int64_t)blockIdx.z * moe_tiles(tokens * p.top_k, p.E) * (32 * p.I);
@@ -292,22 +288,10 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
 // of row r, by lane permutes through the LDS crossbar. Its four dwords go into four MFMAs,
 // eight elements each; the activations follow the same order of K. The scaled conversion to
 // bf16 gives a weight's value exactly.
-constexpr int kUnit = 16;  // blocks
-
-// As loaded by lane l: row l / 4, of every four blocks the block l % 4, and of the 16 scale bytes
-// the dword l % 4.
 struct WeightUnit {
   u32x4 codes[4];
   uint32_t scales;
 };
-// Unit u of a row of nb blocks starts at block max(min(16 u, nb - 16), 0), so that its 16 scale
-// bytes lie in the row. Blocks before 16 u were the unit before's; a row of fewer than 16
-// blocks is one unit, and has no blocks past nb. Those are cleared (clear_unit).
-__device__ __forceinline__ int unit_start(int u, int nb) { return max(min(kUnit * u, nb - kUnit), 0); }
-__device__ __forceinline__ bool unit_cut(int u, int nb) { return kUnit * u + kUnit > nb; }
-// Whether block b (of the row) is one that unit u multiplies.
-__device__ __forceinline__ bool unit_has(int u, int b, int nb) { return b >= kUnit * u && b < nb; }
-
 // Where 16 rows start (the same for the whole wave), and this lane's share of them.
 struct WeightRows {
   const uint8_t *codes, *scales;
@@ -315,8 +299,7 @@ struct WeightRows {
 struct WeightLane {
   uint32_t codes, scales;
   __device__ __forceinline__ WeightLane(int nb, int lane)
-      : codes((uint32_t)(lane >> 2) * (16u * (uint32_t)nb) + 16u * (uint32_t)(lane & 3)),
-        scales((uint32_t)(lane >> 2) * (uint32_t)nb + 4u * (uint32_t)(lane & 3)) {}
+      : codes(weight_code_at(lane, nb)), scales(weight_scale_at(lane, nb)) {}
 };
 __device__ __forceinline__ void load_unit(WeightUnit& w, const WeightRows& rows, const WeightLane& at, int u,
                                           int nb, int lane) {
@@ -327,18 +310,16 @@ __device__ __forceinline__ void load_unit(WeightUnit& w, const WeightRows& rows,
 #pragma unroll
     for (int g = 0; g < 4; ++g) w.codes[g] = *(const u32x4*)&codes[at.codes + 64u * (uint32_t)g];
     __builtin_memcpy(&w.scales, &scales[at.scales], 4);  // at any alignment
-  } else {  // a short row: its last block and byte for those it has not
-    const int part = lane & 3;
-    const uint32_t row = (uint32_t)(lane >> 2) * (uint32_t)nb;
+  } else {
     w.scales = 0u;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      w.codes[g] = *(const u32x4*)&codes[16u * (row + (uint32_t)min(4 * g + part, nb - 1))];
-      w.scales |= (uint32_t)scales[row + (uint32_t)min(4 * part + g, nb - 1)] << (8 * g);
+      w.codes[g] = *(const u32x4*)&codes[short_code_at(lane, g, nb)];
+      w.scales |= (uint32_t)scales[short_scale_at(lane, g, nb)] << (8 * g);
     }
   }
 }
-// Codes and scale bytes of blocks that are not unit u's: zero.
+// Codes and scale bytes of blocks that are not unit u's (unit_cut): zero.
 __device__ __forceinline__ void clear_unit(WeightUnit& w, int u, int nb, int lane) {
   const int b0 = unit_start(u, nb), part = lane & 3;
 #pragma unroll
@@ -361,11 +342,11 @@ template <int kStride>
 __device__ __forceinline__ void load_acts(ActUnit& a, __amdgpu_buffer_rsrc_t window, bool have, uint32_t at,
                                           int u, int nb, int q) {
   if (!have) return;
-  at += (uint32_t)(4 * kStride) * (uint32_t)(unit_start(u, nb) + q);
+  at += act_first(kStride, u, nb, q);
 #pragma unroll
   for (int i = 0; i < kUnit; ++i)
     a.x[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-        window, (int)(at + (uint32_t)kStride * (uint32_t)(16 * (i >> 2) + (i & 3))), 0, 0));
+        window, (int)(at + act_step(kStride, i)), 0, 0));
 }
 __device__ __forceinline__ void clear_acts(ActUnit& a, int u, int nb, int q) {
   const int b0 = unit_start(u, nb);
@@ -551,7 +532,7 @@ __device__ __forceinline__ void store_h(const MoeProblem& p, const ExpertSlots& 
     b[j] = f2u(v);
     rest[j] = (b[j] & 0x7FFFFFFFu) == 0x7F800000u ? 0.0f : v - u2f(b[j] & 0xFFFF0000u);
   }
-  uint8_t* at = s.h + (int64_t)(n / kTileSlots) * (32 * p.I) + ((i >> 3) * 16 + 2 * (n % kTileSlots)) * 16 + 2 * (i & 7);
+  uint8_t* at = s.h + h_at(n, i, p.I);
   *(u32x2*)at = u32x2{(b[0] >> 16) | (b[1] & 0xFFFF0000u), (b[2] >> 16) | (b[3] & 0xFFFF0000u)};
   *(u32x2*)(at + 16) = bf16x4_rne(rest[0], rest[1], rest[2], rest[3]);
 }
@@ -637,18 +618,15 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
   for (int t = 0; t < kT; ++t)
     row0[t] = (uint32_t)(s.slots[min(c0 + 16 * t + r, s.n - 1)] / p.top_k) * (uint32_t)(p.H * 2);
   auto stage = [&](int u, int buf) {
-    const uint32_t from = (uint32_t)unit_start(u, nb) * 64u;
+    const uint32_t from = stage_soff(u, nb);
 #pragma unroll
     for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int k = 0; k < 16 / kGateWaves; ++k) {
         const int row = kGateWaves * k + wave;  // of tile t
         if (c0 + 16 * t + row >= s.n) continue;
-        const int chunk = lane ^ row;
-        // blocks that are not the unit's lie past the window: zeros
-        const uint32_t past = unit_has(u, unit_start(u, nb) + (chunk >> 2), nb) ? 0u : 0x80000000u;
         const uint32_t start = (uint32_t)__builtin_amdgcn_readlane((int)row0[t], row);
-        buffer_load_lds16(rx, lds + buf * kBytes + (16 * t + row) * 1024, (start + 16u * (uint32_t)chunk) | past, from);
+        buffer_load_lds16(rx, lds + buf * kBytes + (16 * t + row) * 1024, stage_voff(start, lane ^ row, u, nb), from);
       }
   };
   const WeightLane at(nb, lane);
@@ -865,15 +843,12 @@ __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
     u32x4 v[kUnit / 4];
   };
   auto fetch = [&](HShare& s, const Item& k, int c) {
-    const int b0 = unit_start(k.u, nb);
     const int64_t tile = __builtin_amdgcn_readfirstlane(s_tile[k.a]) + c;
     const __amdgpu_buffer_rsrc_t rh = make_rsrc(h + tile * (32 * p.I), (uint32_t)(32 * p.I));
 #pragma unroll
     for (int j = 0; j < kUnit / 4; ++j) {
       const int b = 4 * j + wave;  // 1 KiB: a block's four chunks of 16 columns
-      // columns that are not there and blocks that are not the unit's lie past the window: zeros
-      const uint32_t past = kTileSlots * c + (r >> 1) < k.slots && unit_has(k.u, b0 + b, nb) ? 0u : 0x80000000u;
-      s.v[j] = __builtin_amdgcn_raw_buffer_load_b128(rh, (int)((16u * (uint32_t)lane) | past), (b0 + b) * 1024, 0);
+      s.v[j] = __builtin_amdgcn_raw_buffer_load_b128(rh, (int)h_voff(lane, c, k.slots, k.u, b, nb), h_soff(k.u, b, nb), 0);
     }
   };
   auto stage = [&](const HShare& s, int buf) {
