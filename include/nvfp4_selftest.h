@@ -69,6 +69,20 @@ int nvfp4_selftest_bf16_exhaustive(unsigned long long* mismatches, uint32_t* fir
 int nvfp4_selftest_decode(const uint8_t* packed, const uint8_t* scales, uint16_t* hw_f16,
                           uint16_t* sw_f16, int64_t nbytes, void* stream);
 
+/* Which form of its kernels a call launches, for tests that have to reach every one of them. Host
+ * only: no device call; the status of the call itself for sizes that it refuses.
+ *
+ * nvfp4_mxfp4_gemm on num_cus compute units (<= 0: 256): form[0] = nvfp4_mxfp4_kernel, form[1] and
+ * form[2] = rows and columns of its output tiles, form[3] = waves (NVFP4_MXFP4_ROWS) or stage
+ * buffers (the others). nvfp4_mxfp4_linear in one kernel takes the same form of NVFP4_MXFP4_ROWS;
+ * *fused says whether it does. */
+int nvfp4_selftest_mxfp4_form(int64_t M, int64_t N, int64_t K, int num_cus, int form[4], int* fused);
+
+/* nvfp4_mxfp4_moe: form[0] = who routes (0 the first product's workgroups, 1 the plan, 2 a kernel of
+ * its own), form[1] = 1 if the first product stages activations in LDS, form[2] = 1 if in its form of
+ * three workgroups per compute unit, form[3] = shares of the second product (0: without). */
+int nvfp4_selftest_moe_form(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k, int form[4]);
+
 #ifdef __cplusplus
 }
 #endif

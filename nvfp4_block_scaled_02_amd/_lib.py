@@ -76,6 +76,8 @@ SIGNATURES = {
     "nvfp4_selftest_mxfp8_e5m2_exhaustive": (_int, [_vp, _vp, _vp]),
     "nvfp4_selftest_block_scale": (_int, [_vp, _f32, _vp, _vp, _i64, _vp]),
     "nvfp4_selftest_decode": (_int, [_vp, _vp, _vp, _vp, _i64, _vp]),
+    "nvfp4_selftest_mxfp4_form": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int), ctypes.POINTER(_int)]),
+    "nvfp4_selftest_moe_form": (_int, [_i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_int)]),
 }
 
 

@@ -779,4 +779,31 @@ int nvfp4_selftest_decode(const uint8_t* packed, const uint8_t* scales, uint16_t
   return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
 }
 
+int nvfp4_selftest_mxfp4_form(int64_t M, int64_t N, int64_t K, int num_cus, int form[4], int* fused) {
+  if (!form || !fused) return NVFP4_ERROR_INVALID_VALUE;
+  const int s = check_mx4_shape(M, N, K);
+  if (s) return s;
+  if (num_cus <= 0) num_cus = 256;
+  const nvfp4::Mx4Form f = nvfp4::mx4_form(M, N, K, num_cus);
+  form[0] = f.kernel;
+  form[1] = f.m;
+  form[2] = f.n;
+  form[3] = f.depth;
+  *fused = nvfp4::mx4_linear_fused(M, N, K, num_cus);
+  return NVFP4_SUCCESS;
+}
+
+int nvfp4_selftest_moe_form(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k, int form[4]) {
+  if (!form) return NVFP4_ERROR_INVALID_VALUE;
+  if (!moe_sizes(T, E, H) || !moe_sizes(T, E, I) || top_k < 1 || top_k > E ||
+      top_k > nvfp4::kMoeMaxTopK)
+    return NVFP4_ERROR_INVALID_SHAPE;
+  const nvfp4::MoeForm f = nvfp4::moe_form(T, E, H, I, top_k);
+  form[0] = f.routing;
+  form[1] = f.staged;
+  form[2] = f.few;
+  form[3] = f.groups;
+  return NVFP4_SUCCESS;
+}
+
 }  // extern "C"

@@ -141,6 +141,12 @@ hipError_t launch_mx4_dequantize(const void* packed, const void* scales, int64_t
 hipError_t launch_mx4_gemm(const GemmProblem& p, hipStream_t stream, const LaunchInfo& dev);
 // The kernel launch_mx4_gemm picks (a value of nvfp4_mxfp4_kernel).
 int plan_mx4_gemm(int64_t M, int64_t N, int64_t K, int64_t cus);
+// The form of that kernel it launches: output tiles of m x n, and of the kernel for few rows its
+// waves, of the others their stage buffers.
+struct Mx4Form {
+  int kernel, m, n, depth;
+};
+Mx4Form mx4_form(int64_t M, int64_t N, int64_t K, int64_t cus);
 // The linear in one launch, for a few rows: the product's kernel quantizes the bf16
 // activations x itself (and stores the codes and scales).
 bool mx4_linear_fused(int64_t M, int64_t N, int64_t K, int64_t cus);
@@ -172,6 +178,16 @@ int64_t moe_partial_bytes(int64_t T, int64_t H);
 hipError_t launch_moe_router(const void* x, const void* w, int64_t T, int64_t E, int64_t H,
                              void* logits, hipStream_t stream);
 hipError_t launch_moe(const MoeProblem& p, hipStream_t stream);
+// The kernels launch_moe launches: who routes (0: every workgroup of the first product, 1: the plan, 2: a
+// kernel of its own), whether the first product stages activations (64 rows per workgroup), of
+// that the form of three workgroups per compute unit, and the second product's shares (0: the
+// kernel without).
+struct MoeForm {
+  int routing;
+  bool staged, few;
+  int groups;
+};
+MoeForm moe_form(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k);
 
 hipError_t launch_amax(const void* x, int64_t n, float* out, hipStream_t stream,
                        const LaunchInfo& dev);

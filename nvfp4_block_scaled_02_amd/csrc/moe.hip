@@ -991,14 +991,31 @@ hipError_t launch_moe_router(const void* x, const void* w, int64_t T, int64_t E,
   return hipGetLastError();
 }
 
+MoeForm moe_form(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k) {
+  const int64_t chunks = (T + kMoeTokens - 1) / kMoeTokens, slots = (T < kMoeTokens ? T : kMoeTokens) * top_k;
+  const int64_t most = slots < E ? slots : E;  // experts a chunk can reach
+  MoeForm f;
+  f.routing = T <= kInlineTokens ? 0 : T <= 16 ? 1 : 2;
+  // Workgroups of 64 rows, whose waves take all units of K one after the other, where there is one
+  // for each of an MI355X's 256 compute units, with more than 8 units two; else of 16 rows with K over
+  // the waves. (The layer, 16 rows against 64: 4 tokens, 8 of 256 experts, 1024 x 512, 31 us
+  // against 24, 256 workgroups of 64 rows; 3 tokens, 6 of 64, 2048 x 1408, 38 against 34, 396; but
+  // 4 tokens, 2 of 16, 6144 x 2048, 39 against 50, 256; 1 token, 8 of 128, 4096 x 1024, 20 against 28, 128.)
+  f.staged = (I + 63) / 64 * most * chunks >= (H <= 4096 ? 256 : 512);
+  f.few = f.staged && (T <= 16 || (H < 4096 && slots <= 8 * E));
+  f.groups = moe_groups(T, H);
+  return f;
+}
+
 hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   const unsigned chunks = (unsigned)((p.T + kMoeTokens - 1) / kMoeTokens);
   const int64_t slots = (p.T < kMoeTokens ? p.T : kMoeTokens) * p.top_k;
   const unsigned most = (unsigned)(slots < p.E ? slots : p.E);  // experts a chunk can reach
-  const bool in_line = p.T <= kInlineTokens;
+  const MoeForm f = moe_form(p.T, p.E, p.H, p.I, p.top_k);
+  const bool in_line = f.routing == 0;
   hipError_t e;
   if (!in_line) {
-    if (p.T <= 16) {
+    if (f.routing == 1) {
       hipLaunchKernelGGL(moe_plan_kernel<true>, dim3(1), dim3(1024), 0, stream, p);
     } else {
       hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((p.T + 3) / 4)), dim3(256), 0, stream, p);
@@ -1011,15 +1028,9 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   }
   const dim3 wide((unsigned)((p.I + 63) / 64), most, chunks), narrow((unsigned)(p.I / 16), most, chunks);
   const dim3 block(64 * kGateWaves);
-  // Workgroups of 64 rows, whose waves take all units of K one after the other, where there is one
-  // for each of an MI355X's 256 compute units, with more than 8 units two; else of 16 rows with K over
-  // the waves. (The layer, 16 rows against 64: 4 tokens, 8 of 256 experts, 1024 x 512, 31 us
-  // against 24, 256 workgroups of 64 rows; 3 tokens, 6 of 64, 2048 x 1408, 38 against 34, 396; but
-  // 4 tokens, 2 of 16, 6144 x 2048, 39 against 50, 256; 1 token, 8 of 128, 4096 x 1024, 20 against 28, 128.)
-  if ((int64_t)wide.x * wide.y * wide.z >= (p.H <= 4096 ? 256 : 512)) {
+  if (f.staged) {
     if (in_line) hipLaunchKernelGGL((moe_gate_up_kernel<true, true>), wide, block, 0, stream, p);
-    else if (p.T <= 16 || (p.H < 4096 && slots <= 8 * (int64_t)p.E))
-      hipLaunchKernelGGL((moe_gate_up_kernel<false, true>), wide, block, 0, stream, p);
+    else if (f.few) hipLaunchKernelGGL((moe_gate_up_kernel<false, true>), wide, block, 0, stream, p);
     else hipLaunchKernelGGL((moe_gate_up_kernel<false, false>), wide, block, 0, stream, p);
   } else {
     if (in_line) hipLaunchKernelGGL(moe_gate_up_split_kernel<true>, narrow, block, 0, stream, p);
@@ -1027,7 +1038,7 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int groups = moe_groups(p.T, p.H);
+  const int groups = f.groups;
   if (groups == 0) {
     hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(p.H / 16)), dim3(1024), 0, stream, p);
     return hipGetLastError();

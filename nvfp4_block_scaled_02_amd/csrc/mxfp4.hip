@@ -771,22 +771,44 @@ int plan_mx4_gemm(int64_t M, int64_t N, int64_t K, int64_t cus) {
   return best;
 }
 
+Mx4Form mx4_form(int64_t M, int64_t N, int64_t K, int64_t cus) {
+  if (cus <= 0) cus = 256;
+  const int kernel = plan_mx4_gemm(M, N, K, cus);
+  switch (kernel) {
+    case NVFP4_MXFP4_ROWS:
+      // 16 waves for a long K (1 x 8192 x 8192: 9.6 us against 12.2 with 8, but 11.6 against 8.7
+      // for 1 x 14336 x 4096); two weight fragments where one would take a second pass
+      if (M <= 16) return Mx4Form{kernel, 16, 16, K >= 8192 ? 16 : 8};
+      if (M <= 32) return Mx4Form{kernel, 32, N <= 16 * cus ? 16 : 32, 8};
+      return Mx4Form{kernel, 64, 16, 8};
+    case NVFP4_MXFP4_SPLIT64: return Mx4Form{kernel, 64, 64, 3};
+    case NVFP4_MXFP4_TILE64: return Mx4Form{kernel, 64, 64, 4};
+    case NVFP4_MXFP4_TILE64X128: return Mx4Form{kernel, 64, 128, 3};
+    case NVFP4_MXFP4_TILE128:
+      // one workgroup per compute unit: loads four stages ahead (1024 x 4096 x 4096: 16.2 us
+      // against 17.5 with two); more tiles: two workgroups per compute unit (4096 x 4096 x 4096:
+      // 48 against 55 us)
+      return Mx4Form{kernel, 128, 128, ((M + 127) / 128) * ((N + 127) / 128) <= cus ? 4 : 2};
+    case NVFP4_MXFP4_TILE128X256: return Mx4Form{kernel, 128, 256, 3};
+    default: return Mx4Form{kernel, 256, 256, 2};
+  }
+}
+
 hipError_t launch_mx4_gemm(const GemmProblem& p, hipStream_t stream, const LaunchInfo& dev) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
   if (tiles(256, 256) > kMx4MaxTiles) return hipErrorInvalidValue;
 #define NVFP4_MX4_TILE(BM, BN, NBUF, KS)                                                              \
   hipLaunchKernelGGL((gemm_mx4_kernel<BM, BN, NBUF, KS>), dim3((unsigned)tiles(BM, BN)), dim3(256 * KS), 0, \
                      stream, p)
-  switch (plan_mx4_gemm(p.M, p.N, p.K, dev.num_cus)) {
+  const Mx4Form f = mx4_form(p.M, p.N, p.K, dev.num_cus);
+  switch (f.kernel) {
     case NVFP4_MXFP4_ROWS: {
       const size_t lds = (size_t)mx4_rows_lds(p.M, p.K);
-      // 16 waves for a long K (1 x 8192 x 8192: 9.6 us against 12.2 with 8, but 11.6 against 8.7
-      // for 1 x 14336 x 4096); two weight fragments where one would take a second pass
-      if (p.M <= 16) {
-        if (p.K >= 8192) launch_rows<16, 1, 1, false>(p, Mx4Quant{}, lds, stream);
+      if (f.m == 16) {
+        if (f.depth == 16) launch_rows<16, 1, 1, false>(p, Mx4Quant{}, lds, stream);
         else launch_rows<8, 1, 1, false>(p, Mx4Quant{}, lds, stream);
-      } else if (p.M <= 32) {
-        if (p.N <= 16 * (int64_t)dev.num_cus) launch_rows<8, 1, 2, false>(p, Mx4Quant{}, lds, stream);
+      } else if (f.m == 32) {
+        if (f.n == 16) launch_rows<8, 1, 2, false>(p, Mx4Quant{}, lds, stream);
         else launch_rows<8, 2, 2, false>(p, Mx4Quant{}, lds, stream);
       } else {
         launch_rows<8, 1, 4, false>(p, Mx4Quant{}, lds, stream);
@@ -797,10 +819,7 @@ hipError_t launch_mx4_gemm(const GemmProblem& p, hipStream_t stream, const Launc
     case NVFP4_MXFP4_TILE64: NVFP4_MX4_TILE(64, 64, 4, 1); break;
     case NVFP4_MXFP4_TILE64X128: NVFP4_MX4_TILE(64, 128, 3, 1); break;
     case NVFP4_MXFP4_TILE128:
-      // one workgroup per compute unit: loads four stages ahead (1024 x 4096 x 4096: 16.2 us
-      // against 17.5 with two); more tiles: two workgroups per compute unit (4096 x 4096 x 4096:
-      // 48 against 55 us)
-      if (tiles(128, 128) <= dev.num_cus) NVFP4_MX4_TILE(128, 128, 4, 1);
+      if (f.depth == 4) NVFP4_MX4_TILE(128, 128, 4, 1);
       else NVFP4_MX4_TILE(128, 128, 2, 1);
       break;
     case NVFP4_MXFP4_TILE128X256: NVFP4_MX4_TILE(128, 256, 3, 1); break;
@@ -819,7 +838,7 @@ hipError_t launch_mx4_linear_fused(const GemmProblem& p, const void* x, void* pa
                                    hipStream_t stream) {
   const Mx4Quant fq{(const u32x4*)x, (uint32_t*)packed, (uint8_t*)scales};
   const size_t lds = (size_t)(mx4_rows_lds(p.M, p.K) + p.M * (p.K / 2 + 16));
-  if (p.K >= 8192) launch_rows<16, 1, 1, true>(p, fq, lds, stream);
+  if (p.K >= 8192) launch_rows<16, 1, 1, true>(p, fq, lds, stream);  // (as without: mx4_form)
   else launch_rows<8, 1, 1, true>(p, fq, lds, stream);
   return hipGetLastError();
 }

@@ -1,0 +1,25 @@
+"""The sizes of the GPU tests that compare bit for bit reach every form of the MXFP4 product's kernels
+that some size takes (host only)."""
+import random
+
+import test_gpu_mxfp4_forms as product
+from mx4_exact import mxfp4_form
+from nvfp4_block_scaled_02_amd import ops
+
+
+def _log(rng, lo, hi):
+    return int(lo * (hi / lo) ** rng.random())
+
+
+def test_product():
+    rng, seen = random.Random(1), set()
+    for _ in range(100000):
+        seen.add(mxfp4_form(_log(rng, 1, 9000), _log(rng, 1, 20000), 32 * _log(rng, 1, 400))[0])
+    for M, N, K, form in product.CASES:
+        assert mxfp4_form(M, N, K)[0] == form, (M, N, K)
+    assert {c[3] for c in product.CASES} == seen
+    fused = {(c[3], c[4]) for c in product.LINEAR}
+    for M, N, K, form, one in product.LINEAR:
+        assert mxfp4_form(M, N, K) == (form, one), (M, N, K)
+    assert {f for f, one in fused if one} == {(0, 16, 16, 8), (0, 16, 16, 16)}
+    assert len(seen) == 12 and ops.MXFP4_KERNELS.keys() == {f[0] for f in seen}
