@@ -1,9 +1,10 @@
-"""The sizes of the GPU tests that compare bit for bit reach every form of the MXFP4 product's kernels
-that some size takes (host only)."""
+"""The sizes of the GPU tests that compare bit for bit reach every form of the MXFP4 product's and the
+mixture-of-experts layer's kernels that some size takes (host only)."""
 import random
 
+import test_gpu_moe_exact as moe
 import test_gpu_mxfp4_forms as product
-from mx4_exact import mxfp4_form
+from mx4_exact import moe_form, mxfp4_form
 from nvfp4_block_scaled_02_amd import ops
 
 
@@ -23,3 +24,15 @@ def test_product():
         assert mxfp4_form(M, N, K) == (form, one), (M, N, K)
     assert {f for f, one in fused if one} == {(0, 16, 16, 8), (0, 16, 16, 16)}
     assert len(seen) == 12 and ops.MXFP4_KERNELS.keys() == {f[0] for f in seen}
+
+
+def test_layer():
+    rng, seen = random.Random(2), set()
+    for _ in range(100000):
+        T, E = _log(rng, 1, 400), _log(rng, 1, 513)
+        seen.add(moe_form(T, E, rng.randint(1, min(E, 16)), 32 * _log(rng, 1, 200), 32 * _log(rng, 1, 400)))
+    for case in moe.CASES + moe.WIDEST + moe.LARGE:
+        assert moe_form(*case[:5]) == case[5], case
+    assert {c[5] for c in moe.CASES} == seen
+    # the forms of many tokens at more than 64, which are planned in several chunks
+    assert {c[5] for c in moe.CASES if c[0] > 64} == {f for f in seen if f[0] == 2}
