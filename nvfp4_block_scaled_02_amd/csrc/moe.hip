@@ -672,10 +672,12 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
 // For up to 16 tokens (an expert has at most as many slots as there are tokens; 24 layers and
 // numbers, two workgroups against three: 2% less on average, from 8% less to 8% more as the last
 // workgroups fall), and where a workgroup is short, below 8 units of K, and experts have at most 8
-// slots on average. 64 tokens: 4 of 32 experts, 2560 x 1440, the layer 68.5 us against 63.6; 8 of 256,
-// 1024 x 512, 72.7 against 69.5; but 8 of 128, 4096 x 1024, 175 against 179; 4 of 64, 4096 x 1024, 101
-// against 110; and 2 of 8, 4096 x 4096, 76 against 84: an expert of more than 16 slots takes them 32 at
-// a time, with registers that spill.
+// slots on average (an expert of more than 16 takes them 32 at a time, with registers that spill).
+// The layer, two workgroups against three: 64 tokens, 4 of 32 experts, I 1440, with 5, 7, 8 and 8
+// units (H 2560, 3584, 3616, 4096) 77 / 71, 95 / 89, 109 / 106, 102 / 98; 8 of 128, I 1024, with 5, 7, 7, 8
+// and 8 (2560, 3328, 3584, 3616, 4096) 132 / 132, 166 / 167, 170 / 174, 197 / 206, 187 / 193; 6 of 64, I 1408,
+// with 5, 7, 8 and 8 (2560, 3584, 3616, 4064) 113 / 111, 140 / 140, 162 / 168, 174 / 180; and with more slots,
+// 2 of 8, 4096 x 4096, 76 / 84.
 template <bool kInline, bool kFew>
 __global__ void __launch_bounds__(64 * kGateWaves, kFew ? 3 : 2) moe_gate_up_kernel(MoeProblem p) {
   __shared__ __align__(16) uint8_t lds[(kFew ? 2 : kTiles) * 16 * 1024];
@@ -1001,8 +1003,9 @@ MoeForm moe_form(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k) {
   // the waves. (The layer, 16 rows against 64: 4 tokens, 8 of 256 experts, 1024 x 512, 31 us
   // against 24, 256 workgroups of 64 rows; 3 tokens, 6 of 64, 2048 x 1408, 38 against 34, 396; but
   // 4 tokens, 2 of 16, 6144 x 2048, 39 against 50, 256; 1 token, 8 of 128, 4096 x 1024, 20 against 28, 128.)
-  f.staged = (I + 63) / 64 * most * chunks >= (H <= 4096 ? 256 : 512);
-  f.few = f.staged && (T <= 16 || (H < 4096 && slots <= 8 * E));
+  const int64_t units = (H / 32 + kUnit - 1) / kUnit;
+  f.staged = (I + 63) / 64 * most * chunks >= (units <= 8 ? 256 : 512);
+  f.few = f.staged && (T <= 16 || (units < 8 && slots <= 8 * E));
   f.groups = moe_groups(T, H);
   return f;
 }

@@ -36,3 +36,10 @@ def test_layer():
     assert {c[5] for c in moe.CASES} == seen
     # the forms of many tokens at more than 64, which are planned in several chunks
     assert {c[5] for c in moe.CASES if c[0] > 64} == {f for f in seen if f[0] == 2}
+
+
+def test_the_layers_form_goes_by_units():
+    """Widths of the same number of units of 512 elements take the same form of the first product."""
+    for T, E, k, I in ((64, 32, 4, 1440), (64, 128, 8, 1024), (40, 64, 6, 1408), (64, 8, 8, 2048), (4, 16, 2, 2048)):
+        for units in range(1, 14):
+            assert len({moe_form(T, E, k, H, I) for H in range(512 * units - 480, 512 * units + 1, 32)}) == 1, (T, E, units)
