@@ -320,8 +320,9 @@ size_t nvfp4_mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
  * nvfp4_mxfp4_gemm, both on `stream`. The workspace (16-byte aligned, at least
  * nvfp4_mxfp4_linear_workspace_bytes(M, K) bytes) holds the quantized activations on
  * return: packed [M, K/2] at offset 0, scales [M, K/32] at round_up(M*K/2, 256). At most 16
- * rows of together at most 24576 elements run as one kernel, with the same bits in the
- * workspace and the output. Calls that may overlap in time need workspaces of their own.
+ * rows of together at most 24576 elements run as one kernel where there are at most 32 weight
+ * rows per compute unit (N <= 8192 on an MI355X), with the same bits in the workspace and the
+ * output. Calls that may overlap in time need workspaces of their own.
  */
 int nvfp4_mxfp4_linear(const void* x_bf16, const void* w_packed, const void* w_scales, int64_t M,
                        int64_t N, int64_t K, void* out_bf16, void* workspace,

@@ -776,8 +776,10 @@ Mx4Form mx4_form(int64_t M, int64_t N, int64_t K, int64_t cus) {
   const int kernel = plan_mx4_gemm(M, N, K, cus);
   switch (kernel) {
     case NVFP4_MXFP4_ROWS:
-      // 16 waves for a long K (1 x 8192 x 8192: 9.6 us against 12.2 with 8, but 11.6 against 8.7
-      // for 1 x 14336 x 4096); two weight fragments where one would take a second pass
+      // 16 waves for a long K (8 waves against 16, launches in a graph, weights past the caches: 1 x 4096
+      // x 8192 7.8 us / 6.5, 1 x 8192 x 8192 11.5 / 10.8, 1 x 4096 x 14336 10.2 / 9.9, though 1 x 5120 x
+      // 14336 14.5 / 16.1; 1 x 4096 x 7168 6.8 / 6.2, 1 x 8192 x 7168 9.7 / 10.2, 1 x 4096 x 4096
+      // 4.9 / 5.4, 1 x 8192 x 4096 6.4 / 8.6); two weight fragments where one would take a second pass
       if (M <= 16) return Mx4Form{kernel, 16, 16, K >= 8192 ? 16 : 8};
       if (M <= 32) return Mx4Form{kernel, 32, N <= 16 * cus ? 16 : 32, 8};
       return Mx4Form{kernel, 64, 16, 8};

@@ -43,3 +43,12 @@ def test_the_layers_form_goes_by_units():
     for T, E, k, I in ((64, 32, 4, 1440), (64, 128, 8, 1024), (40, 64, 6, 1408), (64, 8, 8, 2048), (4, 16, 2, 2048)):
         for units in range(1, 14):
             assert len({moe_form(T, E, k, H, I) for H in range(512 * units - 480, 512 * units + 1, 32)}) == 1, (T, E, units)
+
+
+def test_linear_in_one_kernel_is_what_the_header_says():
+    rng = random.Random(3)
+    for _ in range(20000):
+        M, N, K = _log(rng, 1, 40), _log(rng, 1, 20000), 32 * _log(rng, 1, 1000)
+        assert mxfp4_form(M, N, K)[1] == (M <= 16 and M * K <= 24576 and N <= 8192), (M, N, K)
+    for M, N, K in ((1, 8192, 24576), (1, 8193, 32), (16, 8192, 1536), (16, 8192, 1568), (17, 64, 32), (1, 1, 24608)):
+        assert mxfp4_form(M, N, K)[1] == (M <= 16 and M * K <= 24576 and N <= 8192), (M, N, K)
