@@ -75,6 +75,8 @@ def _exact(x, chosen, w, k, shift=0):
     xd, u_most = x.double(), 0.0
     power = xd.amax(1, keepdim=True)
     for e in np.unique(chosen.cpu().numpy()).tolist():
+        if e < 0:
+            continue
         t = (chosen == e).any(1).nonzero()[:, 0]
         f = (e + shift) % w[0].shape[0]
         g = 4.0 * xd[t].sum(1, keepdim=True)
@@ -131,3 +133,22 @@ def test_widest(case):
 def test_past_two_to_the_32_bytes(case):
     """512 experts of 8192 x 1024, 4.3 GB of gate and up rows: the first and the last experts chosen."""
     _check(case, used=[0, 1, 255, 256, 510, 511])
+
+
+def test_most_tokens():
+    """2^21 tokens, the largest number taken, as 512 times the same 4096."""
+    E, k, H, I = 4, 2, 32, 32
+    say("moe exact, most tokens")
+    w, x = _weights(E, H, I, k, 32, 1), _activations(4096, H, 32, 7)
+    rng = np.random.default_rng(3)
+    chosen = torch.from_numpy(np.stack([rng.permutation(E)[:k] for _ in range(4096)])).to("cuda")
+    logits = torch.full((4096, E), -200.0, device="cuda").scatter_(1, chosen, 0.0)
+    logits[::7] = -torch.inf   # tokens without experts
+    chosen[::7] = -1
+    exact, steps, _ = _exact(x, chosen, w, k)
+    assert steps < 2.0**24
+    want = exact.float().to(torch.bfloat16)
+    out = torch.full((2**21, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    nv.mxfp4_moe(x.repeat(512, 1), logits.repeat(512, 1), *w, k, renormalize=False, out=out)
+    differ = int((out.view(512, 4096, H) != want).sum())
+    assert differ == 0 and not bool(want[::7].any())
