@@ -784,7 +784,9 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
 // one of `groups` shares of the (expert, unit of K) pairs and writes its fp32 sums by token,
 // which moe_combine_kernel adds. Loads run two items ahead, into three sets of registers: with
 // one ahead a unit's multiplications were all the time its successor's loads had (74 us; now
-// 64, the weights at 4.5 TB/s, and 5 for the sums).
+// 64, the weights at 4.4 TB/s, and 5 for the sums). An expert of more than 8 slots has several
+// tiles of h, multiplied one after the other with the weights in registers (64 tokens, 2 of 8
+// experts, 4096 x 1792, 23 us; the experts' 31 MB take 5).
 constexpr int kSumPitch = 68;  // floats of a token's 64 sums: 16 columns in distinct banks
 
 __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
@@ -964,7 +966,8 @@ int64_t moe_h_bytes(int64_t T, int64_t E, int64_t I, int64_t top_k) {
   return (T + kMoeTokens - 1) / kMoeTokens * moe_tiles(tokens * top_k, E) * (32 * I);
 }
 
-// Shares of the second product's pairs: two workgroups per compute unit, at most kMostGroups (16
+// Shares of the second product's pairs: two workgroups per compute unit (for an MI355X's 256, since the
+// size of the workspace is asked for without a device), at most kMostGroups (16
 // against 8: 64 tokens of 256 experts of 1024 x 512 in 73 us against 91; 32: another 3 less there,
 // 1 to 2 more elsewhere). 0: the kernel without shares, for up to four tokens (five layers of 16
 // to 256 experts, both sides in turn: at 2 and 4 tokens shares are slower in eight of ten, by up
