@@ -288,10 +288,11 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
 // of row r, by lane permutes through the LDS crossbar. Its four dwords go into four MFMAs,
 // eight elements each; the activations follow the same order of K. The scaled conversion to
 // bf16 gives a weight's value exactly.
-struct WeightUnit {
+struct WeightUnit {  // as loaded
   u32x4 codes[4];
   uint32_t scales;
 };
+
 // Where 16 rows start (the same for the whole wave), and this lane's share of them.
 struct WeightRows {
   const uint8_t *codes, *scales;
@@ -409,6 +410,30 @@ __device__ __forceinline__ void multiply_unit(floatx4 (&acc)[kF][kT], const Weig
     // that are not there)
     __builtin_amdgcn_sched_barrier(0);
   }
+}
+
+// The same in two steps, for several tiles in turn: the unit decoded, then each tile's products.
+struct DecodedUnit {
+  bf16x8_t w[kUnit];
+};
+__device__ __forceinline__ void decode_unit(DecodedUnit& d, const WeightUnit& w, int lane) {
+  const int q = lane >> 4, r = lane & 15;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t bytes = from_lane(4 * r + g, w.scales);
+    const float sc = u2f(((bytes >> (8 * q)) & 0xFFu) << 23);
+    const uint32_t c0 = w.codes[g].x, c1 = w.codes[g].y, c2 = w.codes[g].z, c3 = w.codes[g].w;
+    d.w[4 * g] = decode8_bf16(from_lane(4 * r + q, c0), sc);
+    d.w[4 * g + 1] = decode8_bf16(from_lane(4 * r + q, c1), sc);
+    d.w[4 * g + 2] = decode8_bf16(from_lane(4 * r + q, c2), sc);
+    d.w[4 * g + 3] = decode8_bf16(from_lane(4 * r + q, c3), sc);
+  }
+}
+template <typename Fetch>
+__device__ __forceinline__ void multiply_decoded(floatx4& acc, const DecodedUnit& d, const Fetch& fetch) {
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i)
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(d.w[i], __builtin_bit_cast(bf16x8_t, fetch(i)), acc, 0, 0, 0);
 }
 
 constexpr int kTiles = kMoeTokens / 16;
@@ -677,7 +702,7 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
 // units (H 2560, 3584, 3616, 4096) 77 / 71, 95 / 89, 109 / 106, 102 / 98; 8 of 128, I 1024, with 5, 7, 7, 8
 // and 8 (2560, 3328, 3584, 3616, 4096) 132 / 132, 166 / 167, 170 / 174, 197 / 206, 187 / 193; 6 of 64, I 1408,
 // with 5, 7, 8 and 8 (2560, 3584, 3616, 4064) 113 / 111, 140 / 140, 162 / 168, 174 / 180; and with more slots,
-// 2 of 8, 4096 x 4096, 76 / 84.
+// 2 of 8, 4096 x 4096, 93 / 101, 4 of 64, 4096 x 1024, 105 / 115.
 template <bool kInline, bool kFew>
 __global__ void __launch_bounds__(64 * kGateWaves, kFew ? 3 : 2) moe_gate_up_kernel(MoeProblem p) {
   __shared__ __align__(16) uint8_t lds[(kFew ? 2 : kTiles) * 16 * 1024];
@@ -784,9 +809,11 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeProblem p) {
 // one of `groups` shares of the (expert, unit of K) pairs and writes its fp32 sums by token,
 // which moe_combine_kernel adds. Loads run two items ahead, into three sets of registers: with
 // one ahead a unit's multiplications were all the time its successor's loads had (74 us; now
-// 64, the weights at 4.4 TB/s, and 5 for the sums). An expert of more than 8 slots has several
-// tiles of h, multiplied one after the other with the weights in registers (64 tokens, 2 of 8
-// experts, 4096 x 1792, 23 us; the experts' 31 MB take 5).
+// 59, the weights at 4.8 TB/s, and 5 for the sums). An expert of more than 8 slots has several
+// tiles of h, multiplied one after the other with a unit that is permuted and decoded once
+// (against once a tile, the layer: 64 tokens, 8 of 8 experts, 4096 x 4096, 161 -> 137 us; 2 of 8,
+// 4096 x 14336, 266 -> 244), their sums in registers to the expert's end (against adding every unit to
+// the tokens' sums: 138 -> 127, 240 -> 228).
 constexpr int kSumPitch = 68;  // floats of a token's 64 sums: 16 columns in distinct banks
 
 __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
@@ -869,36 +896,36 @@ __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
     // h past the item's first go through a buffer of their own against the same weights.
     Item at = {a_begin, begin - a_begin * nu, slots_of(a_begin)}, then = next(at);
     auto there = [&](const Item& k) { return k.a <= a_end ? k : at; };
-    WeightUnit w0[1], w1[1], w2[1];
+    WeightUnit w0, w1, w2;
     HShare hs, others;
     fetch(hs, at, 0);
-    load(w0[0], at);
+    load(w0, at);
     stage(hs, 0);
     fetch(hs, there(then), 0);
-    load(w1[0], there(then));
-    floatx4 acc[1][1];
-    acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    load(w1, there(then));
+    constexpr int kMost = kMoeTokens / kTileSlots;  // an expert's tiles: a token's slots are of different experts
+    floatx4 acc[kMost];
+#pragma unroll
+    for (int c = 0; c < kMost; ++c) acc[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     auto meet = [&]() {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     };
-    auto multiply = [&](const WeightUnit (&now)[1], int buf) {
-      multiply_unit<1, 1>(acc, now, lane, [&](int i, int) {
-        const int chunk = 16 * (i >> 2) + 4 * q + (i & 3);
-        return *(const u32x4*)&lds[buf * kBytes + (chunk * 16 + r) * 16];
-      });
+    auto h_of = [&](int buf, int i) {
+      const int chunk = 16 * (i >> 2) + 4 * q + (i & 3);
+      return *(const u32x4*)&lds[buf * kBytes + (chunk * 16 + r) * 16];
     };
-    auto add = [&](int c) {  // what acc holds of the item's tile c, to its tokens' sums
+    auto add = [&](int c) {  // the item's tile c to its tokens' sums
       const int s0 = __builtin_amdgcn_readfirstlane(s_first[at.a]);
-      const floatx4 y = add_parts(acc[0][0]);
+      const floatx4 y = add_parts(acc[c]);
       if ((r & 1) == 0 && kTileSlots * c + (r >> 1) < at.slots) {
         const int slot = s_slot[s0 + kTileSlots * c + (r >> 1)];
         *(floatx4*)&sums[(slot / p.top_k) * kSumPitch + 16 * wave + 4 * q] += s_weight[slot] * y;
       }
-      acc[0][0] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      acc[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     };
-    auto turn = [&](WeightUnit (&now)[1], int buf, WeightUnit& fill) {
+    auto turn = [&](WeightUnit& now, int buf, WeightUnit& fill) {
       meet();  // item i's h is in LDS, and everyone is done with item i - 1's
       const Item after = then.a <= a_end ? next(then) : then;
       const int tiles = (at.slots + kTileSlots - 1) / kTileSlots;
@@ -907,24 +934,28 @@ __global__ void __launch_bounds__(256, 2) moe_down_wide_kernel(MoeProblem p) {
       fetch(hs, there(after), 0);
       load(fill, there(after));
       __builtin_amdgcn_sched_barrier(0);
-      if (unit_cut(at.u, nb)) clear_unit(now[0], at.u, nb, lane);
-      multiply(now, buf);
-      // an only tile's units add up in registers
-      if (tiles > 1 || at.u + 1 == u_end(at.a)) add(0);
-      for (int c = 1; c < tiles; ++c) {
+      if (unit_cut(at.u, nb)) clear_unit(now, at.u, nb, lane);
+      DecodedUnit d;
+      decode_unit(d, now, lane);
+      const bool last = at.u + 1 == u_end(at.a);
+      multiply_decoded(acc[0], d, [&](int i) { return h_of(buf, i); });
+      if (last) add(0);
+#pragma unroll
+      for (int c = 1; c < kMost; ++c) {
+        if (c >= tiles) break;
         if (c > 1) meet();
         stage(others, 2);
         meet();
         if (c + 1 < tiles) fetch(others, at, c + 1);
-        multiply(now, 2);
-        add(c);
+        multiply_decoded(acc[c], d, [&](int i) { return h_of(2, i); });
+        if (last) add(c);
       }
       at = then;
       then = after;
       return at.a <= a_end;
     };
-    while (turn(w0, 0, w2[0]) && turn(w1, 1, w0[0]) && turn(w2, 0, w1[0]) &&
-           turn(w0, 1, w2[0]) && turn(w1, 0, w0[0]) && turn(w2, 1, w1[0])) {
+    while (turn(w0, 0, w2) && turn(w1, 1, w0) && turn(w2, 0, w1) &&
+           turn(w0, 1, w2) && turn(w1, 0, w0) && turn(w2, 1, w1)) {
     }
   }
   if (!mine) return;
