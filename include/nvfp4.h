@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_ABI_VERSION 6
+#define NVFP4_ABI_VERSION 7
 
 /* Status codes. All argument validation happens before any HIP call. */
 typedef enum nvfp4_status {
@@ -368,6 +368,93 @@ int nvfp4_mxfp4_moe(const void* x_bf16, const void* logits, const void* w13_pack
                     int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k, int renormalize,
                     void* out_bf16, void* topk_ids, void* topk_weights, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_mxfp4_moe_routed: the same layer with its routing given, as nvfp4_moe_route or the caller's
+ * own rule has it: out[t] = bf16_RNE(sum_j topk_weights[t, j] y_tj). topk_ids int32 [T, top_k] and
+ * topk_weights fp32 [T, top_k] are only read. An id outside [0, E) is no expert and adds nothing;
+ * the same expert twice in a token's row counts once with the sum of its weights. Everything else,
+ * the workspace's size and the limits are nvfp4_mxfp4_moe's.
+ */
+int nvfp4_mxfp4_moe_routed(const void* x_bf16, const void* topk_ids, const void* topk_weights,
+                           const void* w13_packed, const void* w13_scales, const void* w2_packed,
+                           const void* w2_scales, int64_t T, int64_t E, int64_t H, int64_t I,
+                           int64_t top_k, void* out_bf16, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * nvfp4_moe_route: router logits to chosen experts and their weights.
+ *   score_e = softmax(logits)_e over all E (NVFP4_MOE_SOFTMAX) or 1 / (1 + exp(-logit_e))
+ *   (NVFP4_MOE_SIGMOID); key_e = score_e + bias_e (bias fp32 [E], or NULL).
+ *   Of `groups` groups of E / groups consecutive experts the top_groups of largest score stay; a
+ *   group's score is the sum of its group_best (1 or 2) largest keys, of those it has. Of
+ *   their experts the top_k of largest key are chosen, in falling order (without a bias: of
+ *   largest logit). Ties go to the lowest index. Keys and sums are held in 64 bits.
+ *   weight = scale * score, divided by the sum of the chosen scores if renormalize == 1.
+ *   A logit or key of -inf is never chosen; where nothing is left to choose the id is -1 and the
+ *   weight 0 (a row of -inf marks padding). A NaN key ranks first. A NaN logit makes its weight NaN,
+ *   with softmax scores or renormalized weights all of the token's; so does +inf under softmax.
+ *   logits fp32 [T, E] -> ids int32 [T, top_k], weights fp32 [T, top_k]; all 4-byte aligned. T at most
+ *   2^21, E in [1, 512], top_k in [1, min(E, 16)], groups in [1, 64], E % groups == 0, top_groups
+ *   in [1, groups]; scale finite.
+ */
+enum nvfp4_moe_scores { NVFP4_MOE_SOFTMAX = 0, NVFP4_MOE_SIGMOID = 1 };
+int nvfp4_moe_route(const void* logits, const void* bias, int64_t T, int64_t E, int64_t top_k,
+                    int scores, int64_t groups, int64_t top_groups, int group_best, int renormalize,
+                    float scale, void* topk_ids, void* topk_weights, void* stream);
+
+/*
+ * nvfp4_lora: the low-rank adapters of many requests beside a shared projection.
+ *   out[t] = bf16_RNE(y[t] + scales[a] * B[a] (A[a] x[t])), a = adapters[t]; a row whose adapter is
+ *   outside [0, L) has none: out[t] = y[t]. Rows come in any order. Sums in fp32; A[a] x[t] is held
+ *   to 2^-16 of its value for the second product. A row depends on its own adapter alone.
+ *   y_bf16 [T, N] (the projection's output), x_bf16 [T, K], a_bf16 [L, R, K], b_bf16 [L, N, R],
+ *   adapters int32 [T], scales fp32 [L] (NULL: 1), out_bf16 [T, N], which may be y. Adapters of
+ *   smaller rank are padded with zeros.
+ *   R a multiple of 8 up to 128, K a multiple of 8, N any; T at most 2^21, N and K at most 2^20.
+ *   bf16 tensors and workspace 16-byte aligned, adapters and scales 4. The workspace holds at least
+ *   nvfp4_lora_workspace_bytes(T, N, K, R) bytes; calls that may overlap in time need workspaces of
+ *   their own. The result is deterministic for given arguments.
+ */
+size_t nvfp4_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R);
+int nvfp4_lora(const void* y_bf16, const void* x_bf16, const void* a_bf16, const void* b_bf16,
+               const void* adapters, const void* scales, int64_t T, int64_t N, int64_t K, int64_t R,
+               int64_t L, void* out_bf16, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_add_norm: a branch's output through its own norm and gate onto the residual stream, and the
+ * norm ahead of the next branch, whose result is stored as that branch's linear takes it. With
+ * norm(v) = v / sqrt(mean(v^2) + eps) (NVFP4_NORM_RMS) or
+ * (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) (NVFP4_NORM_LAYER), for row m of group g:
+ *   z = y[m], or norm(y[m]) * post_weight;   h[m] = bf16_RNE(x[m] + residual_scale * gate[g] * z);
+ *   n = norm(h[m]) * weight + bias;   n = n * (1 + scale[g]) + shift[g];   out[m] = bf16_RNE(n).
+ * The second norm takes h as stored. Each of post_weight, gate, weight, bias, scale and shift may be
+ * NULL and is then left out; without y, h[m] is x[m], is not written, and post_weight and gate have to
+ * be NULL.
+ *   format: out as bf16 [M, H], or that tensor quantized, byte for byte as nvfp4_quantize (under
+ *   *global_scale_device, if it is not NULL, or global_scale), nvfp4_mxfp4_quantize,
+ *   nvfp4_mxfp8_quantize or nvfp4_fp8r_quantize store it, with its scales.
+ *   x_bf16, y_bf16, h_bf16 [M, H]; h may be x. post_weight, weight and bias bf16 [H]; gate, scale and
+ *   shift bf16 [groups, H]. rows int32 [M]: each row's group; a row whose group is outside
+ *   [0, groups) is not modulated: its scale and shift read as 0, and where there is a gate its h is x.
+ *   rows NULL: M / groups rows each, in their order (M % groups == 0).
+ *   H a multiple of 8 (MXFP4 and MXFP8: 32, NVFP4 and rowwise FP8: 16), at most 32768; eps > 0. All
+ *   bf16 tensors and out 16-byte aligned, rows, scales and global_scale_device 4. Statistics in fp32.
+ */
+enum nvfp4_norm_kind { NVFP4_NORM_RMS = 0, NVFP4_NORM_LAYER = 1 };
+enum nvfp4_norm_format {
+  NVFP4_NORM_BF16 = 0,
+  NVFP4_NORM_NVFP4 = 1,
+  NVFP4_NORM_MXFP4 = 2,
+  NVFP4_NORM_MXFP8 = 3, /* E4M3 elements */
+  NVFP4_NORM_FP8R = 4
+};
+int nvfp4_add_norm(const void* x_bf16, const void* y_bf16, const void* post_weight_bf16,
+                   const void* gate_bf16, float residual_scale, const void* weight_bf16,
+                   const void* bias_bf16, const void* scale_bf16, const void* shift_bf16,
+                   const void* rows, int64_t M, int64_t H, int64_t groups, int kind, float eps,
+                   void* h_bf16, int format, float global_scale, const float* global_scale_device,
+                   void* out, void* scales, void* stream);
 
 /*
  * Rowwise FP8 ("fp8r") path: the other scheme of the "BFL (fp8r / nvfp4)" page (scheme

@@ -15,6 +15,11 @@ Python entry points (thin wrappers over the C ABI in include/nvfp4.h):
 * :func:`mxfp4_gemm_plan` -- which kernel :func:`mxfp4_gemm` runs a shape on (host only)
 * :func:`moe_router`, :func:`mxfp4_moe` -- a mixture-of-experts layer for a few tokens, its
   experts' weights in MXFP4
+* :func:`moe_route`, :func:`mxfp4_moe_routed` -- routing by softmax or sigmoid scores, with a
+  balancing bias and groups of experts, and that layer with its routing given
+* :func:`lora` -- the low-rank adapters of many requests added to a shared projection's output
+* :func:`add_norm` -- residual, gate and norms around a branch in one pass, the result in bf16 or
+  quantized for the next linear
 * :func:`fp8r_quantize`, :func:`fp8r_gemm` -- the rowwise FP8 path
 * :func:`amax`, :func:`calibrate`, :func:`global_scale_from_amax` -- global scales
 * :func:`calibrate_device` -- a global scale kept on the device (quantize, gemm and
@@ -22,6 +27,7 @@ Python entry points (thin wrappers over the C ABI in include/nvfp4.h):
 """
 from ._lib import NVFP4Error, load_library  # noqa: F401
 from .ops import (  # noqa: F401
+    add_norm,
     amax,
     calibrate,
     calibrate_device,
@@ -35,6 +41,9 @@ from .ops import (  # noqa: F401
     linear,
     linear_plan,
     linear_workspace_bytes,
+    lora,
+    lora_workspace_bytes,
+    moe_route,
     moe_router,
     mxfp4_dequantize,
     mxfp4_gemm,
@@ -42,6 +51,7 @@ from .ops import (  # noqa: F401
     mxfp4_linear,
     mxfp4_linear_workspace_bytes,
     mxfp4_moe,
+    mxfp4_moe_routed,
     mxfp4_moe_workspace_bytes,
     mxfp4_quantize,
     mxfp8_gemm,

@@ -11,7 +11,7 @@ import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libnvfp4.so")
-ABI_VERSION = 6
+ABI_VERSION = 7
 
 STATUS = {
     0: "NVFP4_SUCCESS",
@@ -57,6 +57,14 @@ SIGNATURES = {
     "nvfp4_mxfp4_moe_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _i64, _i64]),
     "nvfp4_mxfp4_moe": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int,
                                _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "nvfp4_mxfp4_moe_routed": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp,
+                                      ctypes.c_size_t, _vp]),
+    "nvfp4_moe_route": (_int, [_vp, _vp, _i64, _i64, _i64, _int, _i64, _i64, _int, _int, _f32, _vp, _vp, _vp]),
+    "nvfp4_lora_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _i64]),
+    "nvfp4_lora": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp,
+                          ctypes.c_size_t, _vp]),
+    "nvfp4_add_norm": (_int, [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _f32,
+                              _vp, _int, _f32, _vp, _vp, _vp, _vp]),
     "nvfp4_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "nvfp4_linear": (_int, [_vp, _f32, _vp, _vp, _f32, _i64, _i64, _i64, _vp, _vp,
                             ctypes.c_size_t, _vp]),

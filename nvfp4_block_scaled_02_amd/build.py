@@ -25,7 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnvfp4.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_w4a16.hip", "mxfp8.hip", "fp8r.hip", "amax.hip", "mxfp4.hip",
-           "moe.hip"]
+           "moe.hip", "moe_route.hip", "lora.hip", "norm.hip"]
 ARCH = "gfx950"
 
 

@@ -160,6 +160,12 @@ bool moe_sizes(int64_t T, int64_t E, int64_t width) {
   return T >= 0 && T <= nvfp4::kMoeMaxTokens && E >= 1 && E <= nvfp4::kMoeMaxExperts &&
          width >= 32 && width % 32 == 0 && width <= ((int64_t)1 << 20);
 }
+// Sizes of the low-rank adapters' calls.
+bool lora_sizes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
+  return T >= 0 && T <= nvfp4::kMoeMaxTokens && N >= 0 && N <= ((int64_t)1 << 20) && K >= 8 && K % 8 == 0 &&
+         K <= ((int64_t)1 << 20) && R >= 8 && R % 8 == 0 && R <= nvfp4::kLoraMaxRank && L >= 0 &&
+         L <= 0x7FFFFFFF;
+}
 struct MoeWorkspace {
   size_t ids, weights, plan, h, partial, bytes;  // offsets, and the whole
 };
@@ -503,8 +509,127 @@ int nvfp4_mxfp4_moe(const void* x, const void* logits, const void* w13p, const v
                       (uint16_t*)out, topk_ids ? (int*)topk_ids : (int*)(base + w.ids),
                       topk_weights ? (float*)topk_weights : (float*)(base + w.weights),
                       base + w.plan, base + w.h, (float*)(base + w.partial), T, H, I, (int)E, (int)top_k,
-                      renormalize == 1};
+                      renormalize == 1, nullptr, nullptr};
   hipError_t e = nvfp4::launch_moe(p, (hipStream_t)stream);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+int nvfp4_mxfp4_moe_routed(const void* x, const void* ids, const void* weights, const void* w13p,
+                           const void* w13s, const void* w2p, const void* w2s, int64_t T, int64_t E,
+                           int64_t H, int64_t I, int64_t top_k, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!x || !ids || !weights || !w13p || !w13s || !w2p || !w2s || !out || !workspace)
+    return NVFP4_ERROR_INVALID_VALUE;
+  if (!moe_sizes(T, E, H) || !moe_sizes(T, E, I) || top_k < 1 || top_k > E ||
+      top_k > nvfp4::kMoeMaxTopK)
+    return NVFP4_ERROR_INVALID_SHAPE;
+  if (!aligned(x, 16) || !aligned(w13p, 16) || !aligned(w2p, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(w13s, 4) ||
+      !aligned(w2s, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  const MoeWorkspace w = moe_workspace(T, E, H, I, top_k);
+  if (workspace_bytes < w.bytes) return NVFP4_ERROR_WORKSPACE;
+  if (T == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  int s = current_device(&info);
+  if (s) return s;
+  uint8_t* base = (uint8_t*)workspace;
+  // what is chosen, as the kernels take it (moe_given), goes to the workspace
+  nvfp4::MoeProblem p{(const uint16_t*)x, nullptr, (const uint8_t*)w13p, (const uint8_t*)w13s,
+                      (const uint8_t*)w2p, (const uint8_t*)w2s, (uint16_t*)out, (int*)(base + w.ids),
+                      (float*)(base + w.weights), base + w.plan, base + w.h,
+                      (float*)(base + w.partial), T, H, I, (int)E, (int)top_k, false,
+                      (const int*)ids, (const float*)weights};
+  hipError_t e = nvfp4::launch_moe(p, (hipStream_t)stream);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+int nvfp4_moe_route(const void* logits, const void* bias, int64_t T, int64_t E, int64_t top_k,
+                    int scores, int64_t groups, int64_t top_groups, int group_best, int renormalize,
+                    float scale, void* ids, void* weights, void* stream) {
+  if (!logits || !ids || !weights) return NVFP4_ERROR_INVALID_VALUE;
+  if ((scores != NVFP4_MOE_SOFTMAX && scores != NVFP4_MOE_SIGMOID) || (group_best != 1 && group_best != 2) ||
+      (renormalize != 0 && renormalize != 1) || !isfinite(scale))
+    return NVFP4_ERROR_INVALID_VALUE;
+  if (T < 0 || T > nvfp4::kMoeMaxTokens || E < 1 || E > nvfp4::kMoeMaxExperts || top_k < 1 || top_k > E ||
+      top_k > nvfp4::kMoeMaxTopK || groups < 1 || groups > nvfp4::kRouteMaxGroups || E % groups != 0 ||
+      top_groups < 1 || top_groups > groups)
+    return NVFP4_ERROR_INVALID_SHAPE;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  if (T == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  int s = current_device(&info);
+  if (s) return s;
+  const nvfp4::RouteProblem p{(const float*)logits, (const float*)bias, (int*)ids, (float*)weights, T, (int)E,
+                              (int)top_k, (int)groups, (int)top_groups, group_best,
+                              scores == NVFP4_MOE_SIGMOID, renormalize == 1, scale};
+  hipError_t e = nvfp4::launch_moe_route(p, (hipStream_t)stream);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+// ---- low-rank adapters -------------------------------------------------------------------
+
+size_t nvfp4_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R) {
+  if (!lora_sizes(T, N, K, R, 1)) return 0;
+  return round_up((size_t)nvfp4::lora_down_bytes(T, K, R), 256);
+}
+
+int nvfp4_lora(const void* y, const void* x, const void* a, const void* b, const void* adapters,
+               const void* scales, int64_t T, int64_t N, int64_t K, int64_t R, int64_t L, void* out,
+               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!y || !x || !a || !b || !adapters || !out || !workspace) return NVFP4_ERROR_INVALID_VALUE;
+  if (!lora_sizes(T, N, K, R, L)) return NVFP4_ERROR_INVALID_SHAPE;
+  if (!aligned(y, 16) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 16) || !aligned(adapters, 4) || !aligned(scales, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  if (workspace_bytes < nvfp4_lora_workspace_bytes(T, N, K, R)) return NVFP4_ERROR_WORKSPACE;
+  if (T == 0 || N == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  int s = current_device(&info);
+  if (s) return s;
+  const nvfp4::LoraProblem p{(const uint16_t*)y, (const uint16_t*)x, (const uint16_t*)a, (const uint16_t*)b,
+                             (const int*)adapters, (const float*)scales, (uint16_t*)out, (float*)workspace,
+                             T, N, K, L, (int)R};
+  hipError_t e = nvfp4::launch_lora(p, (hipStream_t)stream);
+  return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
+}
+
+// ---- residual and norm -------------------------------------------------------------------
+
+int nvfp4_add_norm(const void* x, const void* y, const void* post_weight, const void* gate,
+                   float residual_scale, const void* weight, const void* bias, const void* scale,
+                   const void* shift, const void* rows, int64_t M, int64_t H, int64_t groups, int kind,
+                   float eps, void* h, int format, float global_scale,
+                   const float* global_scale_device, void* out, void* scales, void* stream) {
+  if (!x || !out || (y && !h) || (!y && (post_weight || gate))) return NVFP4_ERROR_INVALID_VALUE;
+  if (kind != NVFP4_NORM_RMS && kind != NVFP4_NORM_LAYER) return NVFP4_ERROR_INVALID_VALUE;
+  if (format < NVFP4_NORM_BF16 || format > NVFP4_NORM_FP8R || (format != NVFP4_NORM_BF16 && !scales))
+    return NVFP4_ERROR_INVALID_VALUE;
+  if (!isfinite(eps) || !(eps > 0.0f) || !isfinite(residual_scale)) return NVFP4_ERROR_INVALID_VALUE;
+  if (format == NVFP4_NORM_NVFP4 && !global_scale_device && !valid_scale(global_scale))
+    return NVFP4_ERROR_INVALID_VALUE;
+  const int64_t block = format == NVFP4_NORM_BF16 ? 8 : format == NVFP4_NORM_NVFP4 || format == NVFP4_NORM_FP8R ? 16 : 32;
+  if (M < 0 || M > 0x7FFFFFFF || H < block || H % block != 0 || H > nvfp4::kNormMaxWidth)
+    return NVFP4_ERROR_INVALID_SHAPE;
+  const bool grouped = gate || scale || shift;
+  if (groups < 1 || groups > 0x7FFFFFFF || (grouped && !rows && M % groups != 0)) return NVFP4_ERROR_INVALID_SHAPE;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(post_weight, 16) || !aligned(gate, 16) ||
+      !aligned(weight, 16) || !aligned(bias, 16) || !aligned(scale, 16) || !aligned(shift, 16) ||
+      !aligned(h, 16) || !aligned(out, 16) || !aligned(rows, 4) || !aligned(scales, 4) ||
+      !aligned(global_scale_device, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  if (M == 0) return NVFP4_SUCCESS;
+  nvfp4::LaunchInfo info;
+  int s = current_device(&info);
+  if (s) return s;
+  const nvfp4::NormProblem p{(const uint16_t*)x, (const uint16_t*)y, (const uint16_t*)post_weight,
+                             (const uint16_t*)gate, (const uint16_t*)weight, (const uint16_t*)bias,
+                             (const uint16_t*)scale, (const uint16_t*)shift,
+                             grouped ? (const int*)rows : nullptr, (uint16_t*)h, out, scales, M, H,
+                             grouped ? groups : 1, residual_scale, eps, kind, format, global_scale,
+                             global_scale_device};
+  hipError_t e = nvfp4::launch_add_norm(p, (hipStream_t)stream, info);
   return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);
 }
 

@@ -24,8 +24,8 @@
 // (|x / s| >= 2^-11) that holds when s >= 2^-60, so rows with a smaller scale take the
 // IEEE division instead. The E4M3 encode is gfx950's fp8 conversion, checked exhaustively
 // against the software encoder by the MXFP8 self-test.
-#include "codec.hpp"
 #include "kernels.hpp"
+#include "quant_mx.hpp"
 
 namespace nvfp4 {
 
@@ -35,49 +35,6 @@ __device__ __forceinline__ float wave_max(float a) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) a = __builtin_fmaxf(a, __shfl_xor(a, off, 64));
   return a;
-}
-
-// 8 elements of a row (one bf16x8 word) to 8 E4M3 codes under the row's scale.
-__device__ __forceinline__ u32x2 encode8(const u32x4 v, float s, float r, bool corrected) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x0 = u2f(w[i] << 16), x1 = u2f(w[i] & 0xFFFF0000u);
-    y[2 * i] = corrected ? div_by_scale_unclamped(x0, s, r) : x0 / s;
-    y[2 * i + 1] = corrected ? div_by_scale_unclamped(x1, s, r) : x1 / s;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(y[i], -kE4M3Max, kE4M3Max);
-  uint32_t c0 = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-  c0 = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c0, true);
-  uint32_t c1 = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
-  c1 = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], c1, true);
-  return u32x2{c0, c1};
-}
-
-__device__ __forceinline__ float amax8(const u32x4 v, float a) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a = __builtin_fmaxf(a, __builtin_fabsf(u2f(w[i] << 16)));
-    a = __builtin_fmaxf(a, __builtin_fabsf(u2f(w[i] & 0xFFFF0000u)));
-  }
-  return a;
-}
-
-// Row scale s = RN(amax / 448) (1 for an all-zero row), stored by lane 0.
-struct RowScale {
-  float s, r;
-  bool corrected;
-};
-__device__ __forceinline__ RowScale row_scale(float amax, float* scales, int64_t row, int lane) {
-  RowScale rs;
-  rs.s = amax > 0.0f ? amax / kE4M3Max : 1.0f;  // IEEE division
-  if (lane == 0) scales[row] = rs.s;
-  rs.r = 1.0f / rs.s;
-  rs.corrected = rs.s >= 0x1p-60f;  // wave-uniform
-  return rs;
 }
 
 // Rows of at most 64 * 8 * NR elements, held in registers.

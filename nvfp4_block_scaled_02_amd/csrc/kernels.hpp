@@ -170,6 +170,8 @@ struct MoeProblem {
   int64_t T, H, I;
   int E, top_k;
   bool renormalize;
+  const int* given_ids;         // [T, top_k], or null: the logits are routed
+  const float* given_weights;  // [T, top_k]
 };
 constexpr int64_t kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxTokens = (int64_t)1 << 21;
 int64_t moe_plan_bytes(int64_t T);
@@ -188,6 +190,60 @@ struct MoeForm {
   int groups;
 };
 MoeForm moe_form(int64_t T, int64_t E, int64_t H, int64_t I, int64_t top_k);
+
+// Routing to experts (moe_route.hip): logits fp32 [T, E], bias fp32 [E] or null.
+struct RouteProblem {
+  const float* logits;
+  const float* bias;
+  int* ids;        // [T, top_k]
+  float* weights;  // [T, top_k]
+  int64_t T;
+  int E, top_k, groups, top_groups, group_best;
+  bool sigmoid, renormalize;
+  float scale;
+};
+constexpr int64_t kRouteMaxGroups = 64;
+hipError_t launch_moe_route(const RouteProblem& p, hipStream_t stream);
+
+// Low-rank adapters (lora.hip): out = y + scales[a] * B_a (A_a x), a = adapters[row].
+struct LoraProblem {
+  const uint16_t* y;    // bf16 [T, N]
+  const uint16_t* x;    // bf16 [T, K]
+  const uint16_t* a;    // bf16 [L, R, K]
+  const uint16_t* b;    // bf16 [L, N, R]
+  const int* adapters;  // [T]; outside [0, L): none
+  const float* scales;  // [L], or null: 1
+  uint16_t* out;        // bf16 [T, N]; may be y
+  float* down;          // lora_down_bytes(T, R, K)
+  int64_t T, N, K, L;
+  int R;
+};
+constexpr int64_t kLoraMaxRank = 128;
+int64_t lora_down_bytes(int64_t T, int64_t K, int64_t R);
+hipError_t launch_lora(const LoraProblem& p, hipStream_t stream);
+
+// The fused residual and norm (norm.hip). Null pointers: that part is left out.
+struct NormProblem {
+  const uint16_t* x;     // bf16 [M, H], the residual stream
+  const uint16_t* y;     // bf16 [M, H], a branch's output
+  const uint16_t* post;  // bf16 [H], the weight of the norm of y
+  const uint16_t* gate;  // bf16 [groups, H]
+  const uint16_t* weight;
+  const uint16_t* bias;   // bf16 [H], of the norm of h
+  const uint16_t* scale;  // bf16 [groups, H]
+  const uint16_t* shift;  // bf16 [groups, H]
+  const int* rows;        // [M], a row's group; null: M / groups rows each
+  uint16_t* h;            // bf16 [M, H]; may be x
+  void* out;
+  void* scales;
+  int64_t M, H, groups;
+  float residual_scale, eps;
+  int kind, format;  // nvfp4_norm_kind, nvfp4_norm_format
+  float gs;          // NVFP4: the global scale
+  const float* gs_dev;
+};
+constexpr int64_t kNormMaxWidth = 32768;
+hipError_t launch_add_norm(const NormProblem& p, hipStream_t stream, const LaunchInfo& dev);
 
 hipError_t launch_amax(const void* x, int64_t n, float* out, hipStream_t stream,
                        const LaunchInfo& dev);

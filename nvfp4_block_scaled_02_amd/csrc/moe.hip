@@ -11,6 +11,7 @@
 
 #include "gemm_common.hpp"
 #include "moe_offsets.hpp"
+#include "wave.hpp"
 
 namespace nvfp4 {
 
@@ -23,31 +24,6 @@ constexpr int kMoeTokens = 64;   // tokens planned together
 constexpr int kMoeExperts = (int)kMoeMaxExperts;
 constexpr int kMoeTopK = (int)kMoeMaxTopK;
 constexpr int kMoeSlots = kMoeTokens * kMoeTopK;
-
-// Reductions over a wave in the vector unit (data-parallel primitives: a shift within rows of
-// 16 lanes, then broadcasts across rows); the result is uniform.
-template <int kCtrl, int kRows>
-__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRows, 0xF, false);
-}
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = max(v, dpp_or_zero<0x111, 0xF>(v));  // row_shr 1, 2, 4, 8
-  v = max(v, dpp_or_zero<0x112, 0xF>(v));
-  v = max(v, dpp_or_zero<0x114, 0xF>(v));
-  v = max(v, dpp_or_zero<0x118, 0xF>(v));
-  v = max(v, dpp_or_zero<0x142, 0xA>(v));  // row_bcast 15 into rows 1 and 3
-  v = max(v, dpp_or_zero<0x143, 0xC>(v));  // row_bcast 31 into rows 2 and 3
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  v += u2f(dpp_or_zero<0x111, 0xF>(f2u(v)));
-  v += u2f(dpp_or_zero<0x112, 0xF>(f2u(v)));
-  v += u2f(dpp_or_zero<0x114, 0xF>(f2u(v)));
-  v += u2f(dpp_or_zero<0x118, 0xF>(f2u(v)));
-  v += u2f(dpp_or_zero<0x142, 0xA>(f2u(v)));
-  v += u2f(dpp_or_zero<0x143, 0xC>(f2u(v)));
-  return u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(v), 63));
-}
 
 // ---- the router's product --------------------------------------------------------------
 //
@@ -199,8 +175,35 @@ __device__ __forceinline__ Choice moe_topk(const float* __restrict__ row, int E,
   if (E <= 128) return moe_topk_of<2>(row, E, top_k, renormalize, lane);
   return moe_topk_of<8>(row, E, top_k, renormalize, lane);
 }
+// The choices of a token whose routing the caller gives, likewise. An index that is no expert's is
+// none. One that the token has already is taken into its first slot, with its weight: an
+// expert's slots are of different tokens (which is what bounds them).
+__device__ __forceinline__ Choice moe_given(const MoeProblem& p, int64_t t, int lane) {
+  Choice mine = {-1, 0.0f};
+  if (lane < p.top_k) mine = Choice{p.given_ids[t * p.top_k + lane], p.given_weights[t * p.top_k + lane]};
+  if (mine.id < 0 || mine.id >= p.E) mine = Choice{-1, 0.0f};
+  bool repeated = false;
+  float sum = mine.weight;
+  for (int j = 0; j < p.top_k; ++j) {
+    const int id = __builtin_amdgcn_readlane(mine.id, j);
+    const float weight = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(mine.weight), j));
+    if (id != mine.id || id < 0) continue;
+    if (j < lane) repeated = true;
+    if (j > lane) sum += weight;
+  }
+  return repeated ? Choice{-1, 0.0f} : Choice{mine.id, sum};
+}
+
+// Who routes the tokens of a kernel: the plan that is made already, the kernel itself, the caller.
+enum class Routing { kPlanned, kOwn, kGiven };
+template <Routing kRouting>
+__device__ __forceinline__ Choice choices_of(const MoeProblem& p, int64_t t, int lane) {
+  if constexpr (kRouting == Routing::kGiven) return moe_given(p, t, lane);
+  else return moe_topk(p.logits + t * p.E, p.E, p.top_k, p.renormalize, lane);
+}
+template <Routing kRouting>
 __device__ __forceinline__ void route_token(const MoeProblem& p, int64_t t, int lane, int* chosen) {
-  const Choice c = moe_topk(p.logits + t * p.E, p.E, p.top_k, p.renormalize, lane);
+  const Choice c = choices_of<kRouting>(p, t, lane);
   if (lane < p.top_k) {
     if (chosen) chosen[lane] = c.id;
     p.ids[t * p.top_k + lane] = c.id;
@@ -213,11 +216,12 @@ __device__ __forceinline__ void route_token(const MoeProblem& p, int64_t t, int 
 // against 178; 8 of 256 experts 84 against 73; up to 32 tokens and for few experts alike).
 __global__ void __launch_bounds__(256) moe_route_kernel(MoeProblem p) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t < p.T) route_token(p, t, threadIdx.x & 63, nullptr);
+  if (t < p.T) route_token<Routing::kOwn>(p, t, threadIdx.x & 63, nullptr);
 }
 
-// One workgroup per chunk; kRoute: it routes the tokens itself, one per wave.
-template <bool kRoute>
+// One workgroup per chunk. kOwn: it routes the tokens itself, one per wave (at most 16); kGiven: it
+// takes the caller's routing, up to four tokens per wave.
+template <Routing kRouting>
 __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
   __shared__ int count[kMoeExperts];
   __shared__ int place[kMoeExperts];
@@ -228,8 +232,10 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(MoeProblem p) {
   const int n = nt * p.top_k;
   MoePlan* plan = (MoePlan*)p.plan + blockIdx.x;
   for (int e = threadIdx.x; e < p.E; e += 1024) count[e] = 0;
-  if constexpr (kRoute) {
-    if (wave < nt) route_token(p, t0 + wave, lane, chosen + wave * p.top_k);
+  if constexpr (kRouting == Routing::kOwn) {
+    if (wave < nt) route_token<kRouting>(p, t0 + wave, lane, chosen + wave * p.top_k);
+  } else if constexpr (kRouting == Routing::kGiven) {
+    for (int t = wave; t < nt; t += 16) route_token<kRouting>(p, t0 + t, lane, chosen + t * p.top_k);
   } else {
     for (int i = threadIdx.x; i < n; i += 1024) chosen[i] = p.ids[t0 * p.top_k + i];
   }
@@ -468,11 +474,12 @@ struct InlinePlan {
   float weight[64];
   int slot[kInlineTokens];
 };
+template <Routing kRouting>
 __device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s, InlinePlan& ip, int wave,
                                              int lane) {
   const int T = (int)p.T, n = T * p.top_k;
   if (wave < T) {
-    const Choice c = moe_topk(p.logits + (int64_t)wave * p.E, p.E, p.top_k, p.renormalize, lane);
+    const Choice c = choices_of<kRouting>(p, wave, lane);
     if (lane < p.top_k) {
       ip.id[wave * p.top_k + lane] = c.id;
       ip.weight[wave * p.top_k + lane] = c.weight;
@@ -520,11 +527,11 @@ __device__ __forceinline__ bool expert_slots(const MoeProblem& p, ExpertSlots& s
   s.h = h_tiles(p) + (int64_t)a * (32 * p.I);
   return true;
 }
-template <bool kInline>
+template <Routing kRouting>
 __device__ __forceinline__ bool find_slots(const MoeProblem& p, ExpertSlots& s, int wave, int lane) {
-  if constexpr (kInline) {
+  if constexpr (kRouting != Routing::kPlanned) {
     __shared__ InlinePlan ip;
-    return expert_slots(p, s, ip, wave, lane);
+    return expert_slots<kRouting>(p, s, ip, wave, lane);
   } else {
     return expert_slots(p, s);
   }
@@ -573,14 +580,14 @@ __device__ __forceinline__ floatx4 add_parts(floatx4 v) {
 // h[slot, i] = silu(gate) * up, few experts reached: 16 gate rows and their up rows per
 // workgroup, whose waves take units of K in turn, a unit's weights and activations in flight at
 // once, and meet in LDS.
-template <bool kInline>
+template <Routing kRouting>
 __global__ void __launch_bounds__(64 * kGateWaves, 2) moe_gate_up_split_kernel(MoeProblem p) {
   constexpr int NW = kGateWaves;
   __shared__ floatx4 part[NW][2][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   ExpertSlots s;
-  if (!find_slots<kInline>(p, s, wave, lane)) return;
+  if (!find_slots<kRouting>(p, s, wave, lane)) return;
   const int q = lane >> 4, r = lane & 15;
   const int64_t i0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const int nb = (int)(p.H >> 5), nu = (nb + kUnit - 1) / kUnit;
@@ -703,17 +710,17 @@ __device__ __forceinline__ void gate_up_tiles(const MoeProblem& p, const ExpertS
 // and 8 (2560, 3328, 3584, 3616, 4096) 132 / 132, 166 / 167, 170 / 174, 197 / 206, 187 / 193; 6 of 64, I 1408,
 // with 5, 7, 8 and 8 (2560, 3584, 3616, 4064) 113 / 111, 140 / 140, 162 / 168, 174 / 180; and with more slots,
 // 2 of 8, 4096 x 4096, 93 / 101, 4 of 64, 4096 x 1024, 105 / 115.
-template <bool kInline, bool kFew>
+template <Routing kRouting, bool kFew>
 __global__ void __launch_bounds__(64 * kGateWaves, kFew ? 3 : 2) moe_gate_up_kernel(MoeProblem p) {
   __shared__ __align__(16) uint8_t lds[(kFew ? 2 : kTiles) * 16 * 1024];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   ExpertSlots s;
-  if (!find_slots<kInline>(p, s, wave, lane)) return;
+  if (!find_slots<kRouting>(p, s, wave, lane)) return;
   const int64_t i0 = (int64_t)blockIdx.x * (16 * kGateWaves) + 16 * wave, t0 = (int64_t)blockIdx.z * kMoeTokens;
   const bool mine = i0 < p.I;  // I % 32 == 0: a wave's 16 rows are all there or none
   const GateRows rows(p, s.expert, mine ? i0 : 0);
-  if (kInline || s.n <= 16) {
+  if (kRouting != Routing::kPlanned || s.n <= 16) {
     gate_up_tiles<1, 2>(p, s, rows, mine, t0, i0, 0, wave, lane, lds);
   } else if constexpr (kFew) {
     for (int c0 = 0; c0 < s.n; c0 += 32) {
@@ -1052,26 +1059,31 @@ hipError_t launch_moe(const MoeProblem& p, hipStream_t stream) {
   const bool in_line = f.routing == 0;
   hipError_t e;
   if (!in_line) {
-    if (f.routing == 1) {
-      hipLaunchKernelGGL(moe_plan_kernel<true>, dim3(1), dim3(1024), 0, stream, p);
+    if (p.given_ids != nullptr) {
+      hipLaunchKernelGGL(moe_plan_kernel<Routing::kGiven>, dim3(chunks), dim3(1024), 0, stream, p);
+    } else if (f.routing == 1) {
+      hipLaunchKernelGGL(moe_plan_kernel<Routing::kOwn>, dim3(1), dim3(1024), 0, stream, p);
     } else {
       hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((p.T + 3) / 4)), dim3(256), 0, stream, p);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
-      hipLaunchKernelGGL(moe_plan_kernel<false>, dim3(chunks), dim3(1024), 0, stream, p);
+      hipLaunchKernelGGL(moe_plan_kernel<Routing::kPlanned>, dim3(chunks), dim3(1024), 0, stream, p);
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const dim3 wide((unsigned)((p.I + 63) / 64), most, chunks), narrow((unsigned)(p.I / 16), most, chunks);
   const dim3 block(64 * kGateWaves);
+  const bool given = p.given_ids != nullptr;
   if (f.staged) {
-    if (in_line) hipLaunchKernelGGL((moe_gate_up_kernel<true, true>), wide, block, 0, stream, p);
-    else if (f.few) hipLaunchKernelGGL((moe_gate_up_kernel<false, true>), wide, block, 0, stream, p);
-    else hipLaunchKernelGGL((moe_gate_up_kernel<false, false>), wide, block, 0, stream, p);
+    if (in_line && given) hipLaunchKernelGGL((moe_gate_up_kernel<Routing::kGiven, true>), wide, block, 0, stream, p);
+    else if (in_line) hipLaunchKernelGGL((moe_gate_up_kernel<Routing::kOwn, true>), wide, block, 0, stream, p);
+    else if (f.few) hipLaunchKernelGGL((moe_gate_up_kernel<Routing::kPlanned, true>), wide, block, 0, stream, p);
+    else hipLaunchKernelGGL((moe_gate_up_kernel<Routing::kPlanned, false>), wide, block, 0, stream, p);
   } else {
-    if (in_line) hipLaunchKernelGGL(moe_gate_up_split_kernel<true>, narrow, block, 0, stream, p);
-    else hipLaunchKernelGGL(moe_gate_up_split_kernel<false>, narrow, block, 0, stream, p);
+    if (in_line && given) hipLaunchKernelGGL(moe_gate_up_split_kernel<Routing::kGiven>, narrow, block, 0, stream, p);
+    else if (in_line) hipLaunchKernelGGL(moe_gate_up_split_kernel<Routing::kOwn>, narrow, block, 0, stream, p);
+    else hipLaunchKernelGGL(moe_gate_up_split_kernel<Routing::kPlanned>, narrow, block, 0, stream, p);
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;

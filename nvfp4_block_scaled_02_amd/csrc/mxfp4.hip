@@ -12,6 +12,7 @@
 
 #include "gemm_common.hpp"
 #include "mx4_offsets.hpp"
+#include "quant_mx.hpp"
 
 namespace nvfp4 {
 
@@ -20,53 +21,10 @@ namespace {
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-// Scale byte of a block from the largest bf16 magnitude pattern in it (sign bits cleared):
-// the exponent field less 2, zero for zero and subnormal maxima (whose floor(log2) is at
-// most -127), 0xFF for infinities and NaN.
-__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax16) {
-  const int field = (int)(amax16 >> 7);
-  return field == 0xFF ? 0xFFu : (uint32_t)max(field - 2, 0);
-}
-
-// The scale of byte b as the binary32 operand of gfx950's scaled conversions, which take
-// its exponent field alone: field 0 stands for 2^-127 and field 255 for NaN.
-__device__ __forceinline__ float mx4_scale_operand(uint32_t b) { return u2f(b << 23); }
-
 // ---- quantize ----------------------------------------------------------------------
 //
-// Four lanes share a block: lane 4i+q holds elements [8q, 8q+8) of block i. The block's
-// maximum is taken on the bf16 bit patterns (for magnitudes their integer order is the order
-// of the values), and each lane converts its elements with the scaled conversion from bf16
-// (x / 2^e, nearest even, saturating: equal to the rule above for every bf16 value and
-// scale) into 4 bytes of codes.
-struct Mx4Codes {
-  uint32_t word, byte;
-};
-__device__ __forceinline__ Mx4Codes mx4_encode_quad(const u32x4 v) {
-  uint32_t a = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a = max(a, v[i] & 0x7FFFu);
-    a = max(a, (v[i] >> 16) & 0x7FFFu);
-  }
-  // quad maximum: DPP quad_perm [1,0,3,2], then [2,3,0,1]
-  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, false));
-  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xF, 0xF, false));
-  const uint32_t byte = mx4_scale_byte(a);
-  const float s = mx4_scale_operand(byte);
-  // each pair through an integer of its own: __builtin_bit_cast of a vector's element takes
-  // the first element whatever the index (this toolchain)
-  const uint32_t x0 = v.x, x1 = v.y, x2 = v.z, x3 = v.w;
-  uint32_t w = 0u;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, x0), s, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, x1), s, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, x2), s, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, x3), s, 3);
-  return Mx4Codes{byte == 0xFFu ? 0u : w, byte};  // a NaN block's codes are 0
-}
-
 // Memory-bound: 2 B read, 1/2 + 1/32 B written per element; a lane loads 16 bytes, so that a
-// wave's load reads 1 KiB of consecutive bytes.
+// wave's load reads 1 KiB of consecutive bytes; four lanes share a block (mx4_encode_quad).
 template <int UNROLL>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(const u32x4* __restrict__ x,
                                                            uint32_t* __restrict__ packed,

@@ -18,50 +18,11 @@
 // The same GEMM kernels, with unit block scales and a per-row x per-column scale
 // epilogue, run the rowwise FP8 ("fp8r") product; its quantizer is in fp8r.hip.
 #include "gemm_common.hpp"
+#include "quant_mx.hpp"
 
 namespace nvfp4 {
 
 namespace {
-
-__device__ __forceinline__ void mx_unpack_bf16x8(const u32x4 v, float* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = u2f(w[i] << 16);
-    f[2 * i + 1] = u2f(w[i] & 0xFFFF0000u);
-  }
-}
-
-// x / 2^e clamped to the element type's finite range, [-448, 448] or [-57344, 57344]
-// (sign of zero kept): the conversion below then never overflows, and the clamp is the
-// format's saturation.
-template <bool kE5M2>
-__device__ __forceinline__ float mx_scaled(float x, int e) {
-  constexpr float lim = kE5M2 ? kE5M2Max : kE4M3Max;
-  return __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(x, -e), -lim), lim);
-}
-
-// Shared exponent of a block from its amax (>= 0): floor(log2(amax)) - emax (8 for E4M3,
-// 15 for E5M2) from the binary32 exponent field, clamped to [-127, 127]; zero and
-// binary32-subnormal maxima (floor(log2) <= -127) give -127.
-template <bool kE5M2>
-__device__ __forceinline__ int mx_shared_exponent(float amax) {
-  const int eb = (int)(f2u(amax) >> 23);
-  return eb == 0 ? -127 : max(eb - (kE5M2 ? 142 : 135), -127);
-}
-
-// Four elements y0..y3 (already scaled and clamped) into the element type's bytes
-// 0..3 of a word (round to nearest even).
-template <bool kE5M2>
-__device__ __forceinline__ uint32_t mx_convert4(float y0, float y1, float y2, float y3) {
-  if constexpr (kE5M2) {
-    const uint32_t w = __builtin_amdgcn_cvt_pk_bf8_f32(y0, y1, 0, false);
-    return __builtin_amdgcn_cvt_pk_bf8_f32(y2, y3, w, true);
-  } else {
-    const uint32_t w = __builtin_amdgcn_cvt_pk_fp8_f32(y0, y1, 0, false);
-    return __builtin_amdgcn_cvt_pk_fp8_f32(y2, y3, w, true);
-  }
-}
 
 // ---- quantize ----------------------------------------------------------------------
 //
@@ -88,22 +49,10 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const u32x4* __restric
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       const int64_t li = base + (int64_t)u * blockDim.x;
-      float f[8];
-      mx_unpack_bf16x8(v[u], f);
-      float a = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a = __builtin_fmaxf(a, __builtin_fabsf(f[i]));
-      // quad maximum: lanes 4i..4i+3 (DPP quad_perm [1,0,3,2], then [2,3,0,1])
-      a = __builtin_fmaxf(a, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, a), 0xB1, 0xF, 0xF, false)));
-      a = __builtin_fmaxf(a, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, a), 0x4E, 0xF, 0xF, false)));
-      const int e = mx_shared_exponent<kE5M2>(a);
-      const uint32_t w0 = mx_convert4<kE5M2>(mx_scaled<kE5M2>(f[0], e), mx_scaled<kE5M2>(f[1], e),
-                                             mx_scaled<kE5M2>(f[2], e), mx_scaled<kE5M2>(f[3], e));
-      const uint32_t w1 = mx_convert4<kE5M2>(mx_scaled<kE5M2>(f[4], e), mx_scaled<kE5M2>(f[5], e),
-                                             mx_scaled<kE5M2>(f[6], e), mx_scaled<kE5M2>(f[7], e));
+      const Mx8Codes c = mx8_encode_quad<kE5M2>(v[u]);
       if (li < nlanes) {
-        __builtin_nontemporal_store(u32x2{w0, w1}, &codes[li]);
-        if ((li & 3) == 0) scales[li >> 2] = (uint8_t)(e + 127);
+        __builtin_nontemporal_store(c.words, &codes[li]);
+        if ((li & 3) == 0) scales[li >> 2] = (uint8_t)c.byte;
       }
     }
   }

@@ -446,6 +446,250 @@ def mxfp4_moe(x: torch.Tensor, logits: torch.Tensor, w13_packed: torch.Tensor,
     return (out, ids, weights) if return_routing else out
 
 
+def mxfp4_moe_routed(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_packed: torch.Tensor,
+                     w13_scales: torch.Tensor, w2_packed: torch.Tensor, w2_scales: torch.Tensor,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """:func:`mxfp4_moe` with its routing given: ``ids`` int32 [T, top_k] and ``weights`` fp32
+    [T, top_k], as :func:`moe_route` returns them. An id outside [0, E) is no expert; the same
+    expert twice in a row counts once, with the sum of its weights."""
+    dev = _first(x, "x", torch.bfloat16, 2)
+    _want(ids, "ids", torch.int32, 2, dev)
+    _want(weights, "weights", torch.float32, 2, dev)
+    _want_pair(w13_packed, w13_scales, "w13_", 3, dev)
+    _want_pair(w2_packed, w2_scales, "w2_", 3, dev)
+    if stream is not None or dev != _current_device():
+        with _place(dev, stream):
+            return mxfp4_moe_routed(x, ids, weights, w13_packed, w13_scales, w2_packed, w2_scales, out, workspace)
+    T, H = x.shape
+    E, I2, Hh = w13_packed.shape
+    I, top_k = I2 // 2, ids.shape[1]
+    if ids.shape[0] != T or weights.shape != ids.shape or Hh != H // 2 or I2 != 2 * I or \
+            w13_scales.shape != (E, I2, H // 32) or w2_packed.shape != (E, H, I // 2) or \
+            w2_scales.shape != (E, H, I // 32):
+        raise ValueError("expert weight or routing shapes are inconsistent")
+    lib = _library()
+    if workspace is None:
+        need = lib.nvfp4_mxfp4_moe_workspace_bytes(T, E, H, I, top_k)
+        workspace = x.new_empty((max(need, 1),), dtype=torch.uint8)
+    else:
+        _want(workspace, "workspace", torch.uint8, 1, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _want(out, "out", torch.bfloat16, 2, dev)
+        if out.shape != (T, H):
+            raise ValueError("out shape must be [T, H]")
+    check(lib.nvfp4_mxfp4_moe_routed(x.data_ptr() or _EMPTY, ids.data_ptr() or _EMPTY, weights.data_ptr() or _EMPTY,
+                                     w13_packed.data_ptr() or _EMPTY, w13_scales.data_ptr() or _EMPTY,
+                                     w2_packed.data_ptr() or _EMPTY, w2_scales.data_ptr() or _EMPTY, T, E, H, I, top_k,
+                                     out.data_ptr() or _EMPTY, workspace.data_ptr() or _EMPTY, workspace.numel(),
+                                     _raw_stream(dev)), "nvfp4_mxfp4_moe_routed")
+    return out
+
+
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, scores: str = "softmax",
+              groups: int = 1, top_groups: int | None = None, group_best: int = 1, renormalize: bool = True,
+              scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None, stream=None):
+    """Routing to experts: router ``logits`` (fp32 [T, E], see :func:`moe_router`) -> (ids int32
+    [T, top_k], weights fp32 [T, top_k]) for :func:`mxfp4_moe_routed`.
+
+    ``scores``: "softmax" over all E or "sigmoid". ``bias`` (fp32 [E]) is added to the scores for
+    choosing alone. Of ``groups`` groups of consecutive experts the ``top_groups`` (default: all) with
+    the largest sum of their ``group_best`` (1 or 2) largest scores (with bias) stay. The weights are
+    ``scale`` times the chosen experts' scores, with ``renormalize`` divided by their sum. Ties go
+    to the lowest index; a logit of -inf is never chosen, and what is not there has id -1 and
+    weight 0."""
+    dev = _first(logits, "logits", torch.float32, 2)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, 1, dev)
+    if stream is not None or dev != _current_device():
+        with _place(dev, stream):
+            return moe_route(logits, top_k, bias, scores, groups, top_groups, group_best, renormalize, scale, ids, weights)
+    T, E = logits.shape
+    kind = MOE_SCORES.get(scores)
+    if kind is None:
+        raise ValueError(f"scores must be one of {sorted(MOE_SCORES)}, got {scores!r}")
+    if bias is not None and bias.shape[0] != E:
+        raise ValueError("bias must be [E]")
+    k = max(int(top_k), 0)
+    if ids is None:
+        ids = logits.new_empty((T, k), dtype=torch.int32)
+    else:
+        _want(ids, "ids", torch.int32, 2, dev)
+    if weights is None:
+        weights = logits.new_empty((T, k))
+    else:
+        _want(weights, "weights", torch.float32, 2, dev)
+    if ids.shape != (T, k) or weights.shape != (T, k):
+        raise ValueError("ids and weights must be [T, top_k]")
+    check(_library().nvfp4_moe_route(logits.data_ptr() or _EMPTY, bias.data_ptr() or _EMPTY if bias is not None else None,
+                                     T, E, top_k, kind, groups, groups if top_groups is None else top_groups, group_best,
+                                     1 if renormalize else 0, scale, ids.data_ptr() or _EMPTY,
+                                     weights.data_ptr() or _EMPTY, _raw_stream(dev)), "nvfp4_moe_route")
+    return ids, weights
+
+
+def lora_workspace_bytes(T: int, N: int, K: int, R: int) -> int:
+    return int(load_library().nvfp4_lora_workspace_bytes(T, N, K, R))
+
+
+def lora(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapters: torch.Tensor,
+         scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The low-rank adapters of many requests, added to a shared projection's output ``y`` (bf16 [T, N])
+    of the activations ``x`` (bf16 [T, K]): row t becomes ``y + scales[i] * b[i] @ (a[i] @ x)`` with
+    i = ``adapters[t]`` (int32 [T]); a row whose index is outside [0, L) has no adapter and stays.
+    ``a`` is bf16 [L, R, K], ``b`` bf16 [L, N, R], ``scales`` fp32 [L]. ``out`` may be ``y``."""
+    dev = _first(y, "y", torch.bfloat16, 2)
+    _want(x, "x", torch.bfloat16, 2, dev)
+    _want(a, "a", torch.bfloat16, 3, dev)
+    _want(b, "b", torch.bfloat16, 3, dev)
+    _want(adapters, "adapters", torch.int32, 1, dev)
+    if scales is not None:
+        _want(scales, "scales", torch.float32, 1, dev)
+    if stream is not None or dev != _current_device():
+        with _place(dev, stream):
+            return lora(y, x, a, b, adapters, scales, out, workspace)
+    T, N = y.shape
+    L, R, K = a.shape
+    if x.shape != (T, K) or b.shape != (L, N, R) or adapters.shape[0] != T or \
+            (scales is not None and scales.shape[0] != L):
+        raise ValueError("adapter, activation or output shapes are inconsistent")
+    lib = _library()
+    if workspace is None:
+        need = lib.nvfp4_lora_workspace_bytes(T, N, K, R)
+        workspace = y.new_empty((max(need, 1),), dtype=torch.uint8)
+    else:
+        _want(workspace, "workspace", torch.uint8, 1, dev)
+    if out is None:
+        out = torch.empty_like(y)
+    else:
+        _want(out, "out", torch.bfloat16, 2, dev)
+        if out.shape != (T, N):
+            raise ValueError("out shape must be [T, N]")
+    check(lib.nvfp4_lora(y.data_ptr() or _EMPTY, x.data_ptr() or _EMPTY, a.data_ptr() or _EMPTY, b.data_ptr() or _EMPTY,
+                         adapters.data_ptr() or _EMPTY, scales.data_ptr() or _EMPTY if scales is not None else None,
+                         T, N, K, R, L, out.data_ptr() or _EMPTY, workspace.data_ptr() or _EMPTY, workspace.numel(),
+                         _raw_stream(dev)), "nvfp4_lora")
+    return out
+
+
+NORM_KINDS = {"rms": 0, "layer": 1}
+# name -> (format, bytes of codes per 16 elements, elements per scale: 0 for one fp32 scale per row)
+NORM_FORMATS = {"nvfp4": (1, 8, 16), "mxfp4": (2, 8, 32), "mxfp8": (3, 16, 32), "fp8r": (4, 16, 0)}
+
+
+def add_norm(x: torch.Tensor, y: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+             bias: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+             gate: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+             shift: torch.Tensor | None = None, rows: torch.Tensor | None = None, kind: str = "rms",
+             eps: float = 1e-6, residual_scale: float = 1.0, quantize: str | None = None, global_scale=None,
+             h: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             scales: torch.Tensor | None = None, stream=None):
+    """Residual and norm in one pass: ``h = x + residual_scale * gate * y`` (``y`` through its own norm
+    first where ``post_weight`` is given) and ``n = norm(h) * weight + bias``, then
+    ``n * (1 + scale) + shift``; x, y, h and n bf16 [M, H]. Returns ``(h, n)``.
+
+    ``kind`` is "rms" or "layer". ``weight``, ``bias`` and ``post_weight`` are bf16 [H]; ``gate``,
+    ``scale`` and ``shift`` bf16 [G, H], a row of them for each sequence: ``rows`` (int32 [M]) names
+    each row's, or M / G rows follow one another; a row named outside [0, G) is not modulated and,
+    with a gate, keeps x. Without ``y`` h is x itself. ``h`` may be ``x``.
+
+    ``quantize`` ("nvfp4", "mxfp4", "mxfp8" or "fp8r"): n comes as that format's (codes, scales) pair, byte
+    for byte what :func:`quantize` (under ``global_scale``, a float or a device float32 tensor),
+    :func:`mxfp4_quantize`, :func:`mxfp8_quantize` or :func:`fp8r_quantize` make of it."""
+    dev = _first(x, "x", torch.bfloat16, 2)
+    if stream is not None or dev != _current_device():
+        with _place(dev, stream):
+            return add_norm(x, y, weight, bias, post_weight, gate, scale, shift, rows, kind, eps, residual_scale,
+                            quantize, global_scale, h, out, scales)
+    M, H = x.shape
+    bf16 = torch.bfloat16
+    groups = -1
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is not None:
+            _want(t, name, bf16, 2, dev)
+            if t.shape[1] != H or groups not in (-1, t.shape[0]):
+                raise ValueError("gate, scale and shift must be [G, H]")
+            groups = t.shape[0]
+    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
+        if t is not None:
+            _want(t, name, bf16, 1, dev)
+            if t.shape[0] != H:
+                raise ValueError(f"{name} must be [H]")
+    if rows is not None:
+        _want(rows, "rows", torch.int32, 1, dev)
+        if rows.shape[0] != M:
+            raise ValueError("rows must be [M]")
+    if y is None:
+        if h is not None or gate is not None or post_weight is not None:
+            raise ValueError("h, gate and post_weight need y")
+        h = x
+    else:
+        _want(y, "y", bf16, 2, dev)
+        if h is None:
+            h = torch.empty_like(x)
+        else:
+            _want(h, "h", bf16, 2, dev)
+        if y.shape != (M, H) or h.shape != (M, H):
+            raise ValueError("y and h must be [M, H]")
+    norm = NORM_KINDS.get(kind)
+    if norm is None:
+        raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
+    form, gs, gs_dev = 0, 0.0, None
+    if quantize is None:
+        if scales is not None or global_scale is not None:
+            raise ValueError("scales and global_scale need quantize")
+        if out is None:
+            out = torch.empty_like(x)
+        else:
+            _want(out, "out", bf16, 2, dev)
+            if out.shape != (M, H):
+                raise ValueError("out shape must be [M, H]")
+    else:
+        if quantize not in NORM_FORMATS:
+            raise ValueError(f"quantize must be one of {sorted(NORM_FORMATS)}, got {quantize!r}")
+        form, per16, block = NORM_FORMATS[quantize]
+        if H % (block or 16):
+            raise ValueError(f"H must be a multiple of {block or 16} for {quantize}")
+        if quantize == "nvfp4":
+            gs_dev = _dev_scale(global_scale, "global_scale")
+            if gs_dev is None:
+                gs = float(global_scale)
+            elif gs_dev.get_device() != dev:
+                raise ValueError(f"global_scale is on {gs_dev.device}, x on cuda:{dev}")
+        elif global_scale is not None:
+            raise ValueError("global_scale is NVFP4's")
+        want = (M, H // 16 * per16), ((M, H // block) if block else (M,))
+        kind_of_scales = torch.uint8 if block else torch.float32
+        if out is None:
+            out = x.new_empty(want[0], dtype=torch.uint8)
+        else:
+            _want(out, "out", torch.uint8, 2, dev)
+        if scales is None:
+            scales = x.new_empty(want[1], dtype=kind_of_scales)
+        else:
+            _want(scales, "scales", kind_of_scales, len(want[1]), dev)
+        if out.shape != want[0] or scales.shape != want[1]:
+            raise ValueError(f"out must be {list(want[0])} and scales {list(want[1])}")
+    ptr = _pointer
+    check(_library().nvfp4_add_norm(x.data_ptr() or _EMPTY, ptr(y), ptr(post_weight), ptr(gate), residual_scale,
+                                    ptr(weight), ptr(bias), ptr(scale), ptr(shift), ptr(rows), M, H,
+                                    1 if groups == -1 else groups, norm, eps, h.data_ptr() or _EMPTY, form, gs,
+                                    ptr(gs_dev), out.data_ptr() or _EMPTY, ptr(scales), _raw_stream(dev)),
+          "nvfp4_add_norm")
+    return h, (out if quantize is None else (out, scales))
+
+
+def _pointer(t: torch.Tensor | None):
+    """A tensor's address for the library; None stays what is not there."""
+    return None if t is None else t.data_ptr() or _EMPTY
+
+
 def fp8r_quantize(x: torch.Tensor, codes: torch.Tensor | None = None,
                   scales: torch.Tensor | None = None, stream=None):
     """Rowwise FP8 quantization: bf16 [M, K] -> E4M3 codes uint8 [M, K] + fp32 scales [M]."""
