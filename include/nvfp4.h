@@ -413,8 +413,8 @@ int nvfp4_moe_route(const void* logits, const void* bias, int64_t T, int64_t E, 
  *   smaller rank are padded with zeros.
  *   R a multiple of 8 up to 128, K a multiple of 8, N any; T at most 2^21, N and K at most 2^20.
  *   bf16 tensors and workspace 16-byte aligned, adapters and scales 4. The workspace holds at least
- *   nvfp4_lora_workspace_bytes(T, N, K, R) bytes; calls that may overlap in time need workspaces of
- *   their own. The result is deterministic for given arguments.
+ *   nvfp4_lora_workspace_bytes(T, N, K, R) bytes (0 for few rows, where none is needed and it may be
+ *   NULL); calls that may overlap in time need workspaces of their own. The result is deterministic for given arguments.
  */
 size_t nvfp4_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R);
 int nvfp4_lora(const void* y_bf16, const void* x_bf16, const void* a_bf16, const void* b_bf16,

@@ -572,24 +572,26 @@ int nvfp4_moe_route(const void* logits, const void* bias, int64_t T, int64_t E, 
 
 size_t nvfp4_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R) {
   if (!lora_sizes(T, N, K, R, 1)) return 0;
-  return round_up((size_t)nvfp4::lora_down_bytes(T, K, R), 256);
+  return round_up((size_t)nvfp4::lora_down_bytes(T, N, K, R), 256);
 }
 
 int nvfp4_lora(const void* y, const void* x, const void* a, const void* b, const void* adapters,
                const void* scales, int64_t T, int64_t N, int64_t K, int64_t R, int64_t L, void* out,
                void* workspace, size_t workspace_bytes, void* stream) {
-  if (!y || !x || !a || !b || !adapters || !out || !workspace) return NVFP4_ERROR_INVALID_VALUE;
+  if (!y || !x || !a || !b || !adapters || !out) return NVFP4_ERROR_INVALID_VALUE;
   if (!lora_sizes(T, N, K, R, L)) return NVFP4_ERROR_INVALID_SHAPE;
+  const size_t need = nvfp4_lora_workspace_bytes(T, N, K, R);
+  if (need > 0 && !workspace) return NVFP4_ERROR_INVALID_VALUE;
   if (!aligned(y, 16) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) ||
       !aligned(workspace, 16) || !aligned(adapters, 4) || !aligned(scales, 4))
     return NVFP4_ERROR_MISALIGNED;
-  if (workspace_bytes < nvfp4_lora_workspace_bytes(T, N, K, R)) return NVFP4_ERROR_WORKSPACE;
+  if (workspace_bytes < need) return NVFP4_ERROR_WORKSPACE;
   if (T == 0 || N == 0) return NVFP4_SUCCESS;
   nvfp4::LaunchInfo info;
   int s = current_device(&info);
   if (s) return s;
   const nvfp4::LoraProblem p{(const uint16_t*)y, (const uint16_t*)x, (const uint16_t*)a, (const uint16_t*)b,
-                             (const int*)adapters, (const float*)scales, (uint16_t*)out, (float*)workspace,
+                             (const int*)adapters, (const float*)scales, (uint16_t*)out, (uint16_t*)workspace,
                              T, N, K, L, (int)R};
   hipError_t e = nvfp4::launch_lora(p, (hipStream_t)stream);
   return e == hipSuccess ? NVFP4_SUCCESS : hip_fail(e);

@@ -214,12 +214,12 @@ struct LoraProblem {
   const int* adapters;  // [T]; outside [0, L): none
   const float* scales;  // [L], or null: 1
   uint16_t* out;        // bf16 [T, N]; may be y
-  float* down;          // lora_down_bytes(T, R, K)
+  uint16_t* down;       // lora_down_bytes(T, N, K, R): A x, two bf16 parts
   int64_t T, N, K, L;
   int R;
 };
 constexpr int64_t kLoraMaxRank = 128;
-int64_t lora_down_bytes(int64_t T, int64_t K, int64_t R);
+int64_t lora_down_bytes(int64_t T, int64_t N, int64_t K, int64_t R);
 hipError_t launch_lora(const LoraProblem& p, hipStream_t stream);
 
 // The fused residual and norm (norm.hip). Null pointers: that part is left out.

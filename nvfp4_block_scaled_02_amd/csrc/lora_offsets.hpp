@@ -7,21 +7,57 @@
 namespace nvfp4 {
 namespace {
 
-// First step of K (32 elements) of split i of n.
-NVFP4_HD int lora_split_begin(int steps, int i, int n) { return (int)((int64_t)steps * i / n); }
-
 // Column of the output, within a wave's 64, of row r (0..15) of its fragment i (0..3) of B: a lane's results
 // of fragment i are rows 4q .. 4q + 3, columns 16q + 4i .. + 3.
 NVFP4_HD int lora_column(int r, int i) { return 16 * (r >> 2) + 4 * i + (r & 3); }
 
-// Parts of K: as many as bring the first product's workgroups to 256, at least 8 steps each.
-NVFP4_HD int64_t lora_splits(int64_t T, int64_t K) {
-  const int64_t tiles = (T + 15) / 16, most = (K + 255) / 256, want = (256 + tiles - 1) / (tiles > 0 ? tiles : 1);
-  return want < 1 ? 1 : want > most ? most : want;
+// The two parts of v along the matrix instruction's K: chunk c (8 elements) of 2R is chunk c % (R / 8) of
+// the upper parts, then of the lower. Whether step k (four chunks) multiplies the same rows of B
+// as step k - R / 32: where R is a multiple of 32.
+NVFP4_HD bool lora_halves(int R) { return R % 32 == 0; }
+NVFP4_HD int lora_steps(int R) { return (R + 15) / 16; }
+
+// Staging a unit of kC chunks (16 bytes each) of a row: the k-th load of 64 lanes takes rows
+// k * 64 / kC and on, lane l the chunk that its slot l % kC holds of row k * 64 / kC + l / kC. Per-lane
+// offset from row `first` of the operand on (chunks past the row lie past any window); the unit
+// itself is in the scalar offset.
+template <int kC>
+NVFP4_HD uint32_t lora_stage_voff(int lane, int k, int first, uint32_t pitch, int unit, int chunks) {
+  const int row = k * (64 / kC) + lane / kC, chunk = (lane % kC) ^ (row & 15);
+  return ((uint32_t)(first + row) * pitch + 16u * (uint32_t)chunk) | (unit * kC + chunk < chunks ? 0u : 0x80000000u);
 }
 
-// Workgroups that share the distinct adapters of 16 rows.
-NVFP4_HD int64_t lora_deal(int64_t T) { return T <= 256 ? (T < 16 ? (T > 0 ? T : 1) : 16) : 1; }
+// Which of n neighbours a workgroup takes: consecutive workgroups go to the 8 XCDs in turn, and each XCD
+// gets neighbours, which mostly share an adapter, for its own level-2 cache. (The first n % 8 XCDs
+// have one more.)
+NVFP4_HD int64_t lora_neighbour(int64_t i, int64_t n) {
+  const int64_t xcd = i % 8, each = n / 8, more = n % 8;
+  return xcd * each + (xcd < more ? xcd : more) + i / 8;
+}
+
+// The form of the first product: within the second's kernel, with one or two fragments of 16 ranks
+// per tile of rows, or for many rows at once.
+enum class LoraDown { kFused, kNarrow, kPair, kWide };
+struct LoraForm {
+  LoraDown down;
+  int deal;      // its workgroups that share the distinct adapters of a tile of 16 rows
+  int up_deal;   // the second product's
+  int up_tiles;  // tiles of 16 rows per workgroup of the second product
+};
+NVFP4_HD int64_t lora_clamp(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+NVFP4_HD LoraForm lora_form(int64_t T, int64_t N, int64_t K, int64_t R) {
+  const int64_t tiles = (T + 15) / 16, slices = (N + 511) / 512, parts = (R + 15) / 16, most = T < 16 ? T : 16;
+  LoraForm f;
+  if (tiles < 1 || slices < 1) return LoraForm{LoraDown::kFused, 1, 1, 1};
+  if (R <= 32 && (tiles * slices <= 16 || (slices == 1 && tiles <= 64)))
+    return LoraForm{LoraDown::kFused, (int)lora_clamp(256 / (tiles * slices), 1, most), 1, 1};
+  f.down = R <= 16 || tiles * parts <= 256 ? LoraDown::kNarrow : R <= 32 || T <= 4096 ? LoraDown::kPair : LoraDown::kWide;
+  f.deal = f.down == LoraDown::kWide ? 1 : (int)lora_clamp(1024 / (tiles * parts), 1, most);
+  const int64_t work = tiles * ((N + 255) / 256);
+  f.up_deal = (int)lora_clamp(512 / work, 1, most);
+  f.up_tiles = (int)lora_clamp(work / 2048, 1, 16);
+  return f;
+}
 
 }  // namespace
 }  // namespace nvfp4

@@ -562,9 +562,11 @@ def lora(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ada
     lib = _library()
     if workspace is None:
         need = lib.nvfp4_lora_workspace_bytes(T, N, K, R)
-        workspace = y.new_empty((max(need, 1),), dtype=torch.uint8)
+        if need:  # (few rows need none)
+            workspace = y.new_empty((need,), dtype=torch.uint8)
     else:
         _want(workspace, "workspace", torch.uint8, 1, dev)
+        need = workspace.numel()
     if out is None:
         out = torch.empty_like(y)
     else:
@@ -573,8 +575,7 @@ def lora(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ada
             raise ValueError("out shape must be [T, N]")
     check(lib.nvfp4_lora(y.data_ptr() or _EMPTY, x.data_ptr() or _EMPTY, a.data_ptr() or _EMPTY, b.data_ptr() or _EMPTY,
                          adapters.data_ptr() or _EMPTY, scales.data_ptr() or _EMPTY if scales is not None else None,
-                         T, N, K, R, L, out.data_ptr() or _EMPTY, workspace.data_ptr() or _EMPTY, workspace.numel(),
-                         _raw_stream(dev)), "nvfp4_lora")
+                         T, N, K, R, L, out.data_ptr() or _EMPTY, _pointer(workspace), need, _raw_stream(dev)), "nvfp4_lora")
     return out
 
 

@@ -182,5 +182,6 @@ def test_refusals():
             nv.lora(*bad)
     with pytest.raises(nv.NVFP4Error):
         nv.lora(y, x, a[:, :4].contiguous(), b[:, :, :4].contiguous(), ad)
+    y, x, a, b, s = _inputs(4, 32, 64, 40, 2, 1)
     with pytest.raises(nv.NVFP4Error):
         nv.lora(y, x, a, b, ad, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
