@@ -24,7 +24,8 @@ def _check(l, k, **how):
     assert nv.moe_route(l, k, ids=ids, weights=weights, **how)[0] is ids
     bias = how.pop("bias", None)
     wid, wwt = BO.route(to_host(l), k, bias=None if bias is None else to_host(bias), **how)
-    assert np.array_equal(to_host(ids), wid)
+    bad = np.flatnonzero((to_host(ids) != wid).any(1))
+    assert bad.size == 0, f"rows {bad[:5]}: {to_host(ids)[bad[:5]].tolist()} for {wid[bad[:5]].tolist()}"
     got = to_host(weights).astype(np.float64)
     assert np.array_equal(np.isnan(got), np.isnan(wwt))
     fine = ~np.isnan(wwt)
@@ -148,3 +149,32 @@ def test_refusals():
         nv.moe_route(l.half(), 2)
     with pytest.raises(ValueError):
         nv.moe_route(l.t(), 2)
+
+
+def _next(x, n):
+    """x moved by n steps of fp32."""
+    return float((np.float32(x).view(np.int32) + n).view(np.float32)) if x > 0 else -_next(-x, -n)
+
+
+@pytest.mark.parametrize("E,groups,top", [(16, 1, 1), (60, 1, 1), (64, 4, 2), (160, 8, 3), (256, 8, 4), (512, 16, 5), (96, 12, 4)])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_neighbours_a_few_steps_apart(E, groups, top, scores):
+    """Rows whose first, second, last and next choices lie one to a few hundred steps of fp32 apart, in either order
+    of index, alone and in runs: where 32-bit keys do not tell."""
+    k = 6
+    rows = []
+    r = np.random.default_rng(E)
+    for trial in range(64):
+        l = r.standard_normal(E).astype(np.float32)
+        order = np.argsort(-l)
+        for at in ((0,), (k - 2,), (k - 1,), (k,), (0, k - 1), (k - 1, k), (k - 1, k, k + 1), tuple(range(k + 2)))[trial % 8]:
+            if at + 1 < E:
+                step = int(r.choice([0, 1, 2, 7, 30, 300])) * int(r.choice([-1, 1]))
+                l[order[at + 1]] = _next(float(l[order[at]]), step) if l[order[at]] != 0 else 0.0
+        rows.append(l)
+    l = torch.from_numpy(np.stack(rows)).cuda()
+    bias = torch.from_numpy((0.05 * r.standard_normal(E)).astype(np.float32)).cuda()
+    flat = torch.full((E,), 0.125, device="cuda")  # every key moved alike: neighbours stay neighbours
+    for b in (None, flat, bias):
+        for best in (1, 2):
+            _check(l, k, scores=scores, bias=b, groups=groups, top_groups=top, group_best=best, renormalize=best == 1)
