@@ -575,7 +575,8 @@ def lora(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ada
             raise ValueError("out shape must be [T, N]")
     check(lib.nvfp4_lora(y.data_ptr() or _EMPTY, x.data_ptr() or _EMPTY, a.data_ptr() or _EMPTY, b.data_ptr() or _EMPTY,
                          adapters.data_ptr() or _EMPTY, scales.data_ptr() or _EMPTY if scales is not None else None,
-                         T, N, K, R, L, out.data_ptr() or _EMPTY, _pointer(workspace), need, _raw_stream(dev)), "nvfp4_lora")
+                         T, N, K, R, L, out.data_ptr() or _EMPTY,
+                         None if workspace is None else workspace.data_ptr() or _EMPTY, need, _raw_stream(dev)), "nvfp4_lora")
     return out
 
 
@@ -609,19 +610,15 @@ def add_norm(x: torch.Tensor, y: torch.Tensor | None = None, weight: torch.Tenso
             return add_norm(x, y, weight, bias, post_weight, gate, scale, shift, rows, kind, eps, residual_scale,
                             quantize, global_scale, h, out, scales)
     M, H = x.shape
-    bf16 = torch.bfloat16
-    groups = -1
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is not None:
-            _want(t, name, bf16, 2, dev)
-            if t.shape[1] != H or groups not in (-1, t.shape[0]):
-                raise ValueError("gate, scale and shift must be [G, H]")
-            groups = t.shape[0]
-    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
-        if t is not None:
-            _want(t, name, bf16, 1, dev)
-            if t.shape[0] != H:
-                raise ValueError(f"{name} must be [H]")
+    groups = 1
+    if gate is not None or scale is not None or shift is not None:
+        groups = _group_vectors(gate, scale, shift, H, dev)
+    if weight is not None:
+        _width_vector(weight, "weight", H, dev)
+    if bias is not None:
+        _width_vector(bias, "bias", H, dev)
+    if post_weight is not None:
+        _width_vector(post_weight, "post_weight", H, dev)
     if rows is not None:
         _want(rows, "rows", torch.int32, 1, dev)
         if rows.shape[0] != M:
@@ -631,64 +628,89 @@ def add_norm(x: torch.Tensor, y: torch.Tensor | None = None, weight: torch.Tenso
             raise ValueError("h, gate and post_weight need y")
         h = x
     else:
-        _want(y, "y", bf16, 2, dev)
+        _want(y, "y", torch.bfloat16, 2, dev)
         if h is None:
             h = torch.empty_like(x)
         else:
-            _want(h, "h", bf16, 2, dev)
-        if y.shape != (M, H) or h.shape != (M, H):
+            _want(h, "h", torch.bfloat16, 2, dev)
+        if y.shape != x.shape or h.shape != x.shape:
             raise ValueError("y and h must be [M, H]")
     norm = NORM_KINDS.get(kind)
     if norm is None:
         raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
     form, gs, gs_dev = 0, 0.0, None
-    if quantize is None:
-        if scales is not None or global_scale is not None:
-            raise ValueError("scales and global_scale need quantize")
-        if out is None:
-            out = torch.empty_like(x)
-        else:
-            _want(out, "out", bf16, 2, dev)
-            if out.shape != (M, H):
-                raise ValueError("out shape must be [M, H]")
+    if quantize is not None:
+        form, gs, gs_dev, out, scales = _quantized_norm(x, quantize, global_scale, out, scales, dev)
+    elif scales is not None or global_scale is not None:
+        raise ValueError("scales and global_scale need quantize")
+    elif out is None:
+        out = torch.empty_like(x)
     else:
-        if quantize not in NORM_FORMATS:
-            raise ValueError(f"quantize must be one of {sorted(NORM_FORMATS)}, got {quantize!r}")
-        form, per16, block = NORM_FORMATS[quantize]
-        if H % (block or 16):
-            raise ValueError(f"H must be a multiple of {block or 16} for {quantize}")
-        if quantize == "nvfp4":
-            gs_dev = _dev_scale(global_scale, "global_scale")
-            if gs_dev is None:
-                gs = float(global_scale)
-            elif gs_dev.get_device() != dev:
-                raise ValueError(f"global_scale is on {gs_dev.device}, x on cuda:{dev}")
-        elif global_scale is not None:
-            raise ValueError("global_scale is NVFP4's")
-        want = (M, H // 16 * per16), ((M, H // block) if block else (M,))
-        kind_of_scales = torch.uint8 if block else torch.float32
-        if out is None:
-            out = x.new_empty(want[0], dtype=torch.uint8)
-        else:
-            _want(out, "out", torch.uint8, 2, dev)
-        if scales is None:
-            scales = x.new_empty(want[1], dtype=kind_of_scales)
-        else:
-            _want(scales, "scales", kind_of_scales, len(want[1]), dev)
-        if out.shape != want[0] or scales.shape != want[1]:
-            raise ValueError(f"out must be {list(want[0])} and scales {list(want[1])}")
-    ptr = _pointer
-    check(_library().nvfp4_add_norm(x.data_ptr() or _EMPTY, ptr(y), ptr(post_weight), ptr(gate), residual_scale,
-                                    ptr(weight), ptr(bias), ptr(scale), ptr(shift), ptr(rows), M, H,
-                                    1 if groups == -1 else groups, norm, eps, h.data_ptr() or _EMPTY, form, gs,
-                                    ptr(gs_dev), out.data_ptr() or _EMPTY, ptr(scales), _raw_stream(dev)),
-          "nvfp4_add_norm")
+        _want(out, "out", torch.bfloat16, 2, dev)
+        if out.shape != x.shape:
+            raise ValueError("out shape must be [M, H]")
+    check(_library().nvfp4_add_norm(x.data_ptr() or _EMPTY, None if y is None else y.data_ptr() or _EMPTY,
+                                    None if post_weight is None else post_weight.data_ptr() or _EMPTY,
+                                    None if gate is None else gate.data_ptr() or _EMPTY, residual_scale,
+                                    None if weight is None else weight.data_ptr() or _EMPTY,
+                                    None if bias is None else bias.data_ptr() or _EMPTY,
+                                    None if scale is None else scale.data_ptr() or _EMPTY,
+                                    None if shift is None else shift.data_ptr() or _EMPTY,
+                                    None if rows is None else rows.data_ptr() or _EMPTY, M, H, groups, norm, eps,
+                                    h.data_ptr() or _EMPTY, form, gs, None if gs_dev is None else gs_dev.data_ptr(),
+                                    out.data_ptr() or _EMPTY, None if scales is None else scales.data_ptr() or _EMPTY,
+                                    _raw_stream(dev)), "nvfp4_add_norm")
     return h, (out if quantize is None else (out, scales))
 
 
-def _pointer(t: torch.Tensor | None):
-    """A tensor's address for the library; None stays what is not there."""
-    return None if t is None else t.data_ptr() or _EMPTY
+def _width_vector(t: torch.Tensor, name: str, H: int, dev: int):
+    _want(t, name, torch.bfloat16, 1, dev)
+    if t.shape[0] != H:
+        raise ValueError(f"{name} must be [H]")
+
+
+def _group_vectors(gate, scale, shift, H: int, dev: int) -> int:
+    """Checks add_norm's vectors of groups; how many groups they have."""
+    groups = -1
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is not None:
+            _want(t, name, torch.bfloat16, 2, dev)
+            if t.shape[1] != H or groups not in (-1, t.shape[0]):
+                raise ValueError("gate, scale and shift must be [G, H]")
+            groups = t.shape[0]
+    return groups
+
+
+def _quantized_norm(x, quantize: str, global_scale, out, scales, dev: int):
+    """add_norm's format number, global scale (a float, and a device tensor or None), codes and scales."""
+    if quantize not in NORM_FORMATS:
+        raise ValueError(f"quantize must be one of {sorted(NORM_FORMATS)}, got {quantize!r}")
+    M, H = x.shape
+    form, per16, block = NORM_FORMATS[quantize]
+    if H % (block or 16):
+        raise ValueError(f"H must be a multiple of {block or 16} for {quantize}")
+    gs, gs_dev = 0.0, None
+    if quantize == "nvfp4":
+        gs_dev = _dev_scale(global_scale, "global_scale")
+        if gs_dev is None:
+            gs = float(global_scale)
+        elif gs_dev.get_device() != dev:
+            raise ValueError(f"global_scale is on {gs_dev.device}, x on cuda:{dev}")
+    elif global_scale is not None:
+        raise ValueError("global_scale is NVFP4's")
+    want = (M, H // 16 * per16), ((M, H // block) if block else (M,))
+    kind = torch.uint8 if block else torch.float32
+    if out is None:
+        out = x.new_empty(want[0], dtype=torch.uint8)
+    else:
+        _want(out, "out", torch.uint8, 2, dev)
+    if scales is None:
+        scales = x.new_empty(want[1], dtype=kind)
+    else:
+        _want(scales, "scales", kind, len(want[1]), dev)
+    if out.shape != want[0] or scales.shape != want[1]:
+        raise ValueError(f"out must be {list(want[0])} and scales {list(want[1])}")
+    return form, gs, gs_dev, out, scales
 
 
 def fp8r_quantize(x: torch.Tensor, codes: torch.Tensor | None = None,
