@@ -252,7 +252,8 @@ struct UpWeights {
 #pragma unroll
       for (int k = 0; k < kW; ++k) {
         const int c = 4 * k + q;
-        w[k][i] = c < 2 * R8 ? from[c % R8] : u32x4{0u, 0u, 0u, 0u};
+        w[k][i] = from[c % R8];
+        if (p.R % 16 != 0 && c >= 2 * R8) w[k][i] = u32x4{0u, 0u, 0u, 0u};
       }
     }
   }
@@ -276,8 +277,9 @@ struct UpWeights {
 
 // The sums pass through LDS, so that y is read and out written in whole pieces of 128 kWaves bytes of
 // a row (each lane with the columns that the matrix instruction gives it: 16 rows in every access,
-// 16384 x 4096 of rank 16 77 us instead of 63). A thread has 8 columns of two rows of a tile.
-template <int kWaves>
+// 16384 x 4096 of rank 16 77 us instead of 63). A thread has 8 columns of two rows of a tile. kWhole: N
+// is a multiple of 8, and the loads have no branch around them that would wait for them.
+template <int kWaves, bool kWhole>
 struct UpRows {
   static constexpr int kPitch = 64 * kWaves + 4;  // floats
   const int row, column;
@@ -290,15 +292,20 @@ struct UpRows {
   __device__ __forceinline__ void load(const LoraProblem& p, int64_t t0, uint32_t wanted) {  // a bit per row
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (((wanted >> (row + 8 * i)) & 1) == 0) continue;
-      const uint16_t* from = p.y + min(t0 + row + 8 * i, p.T - 1) * p.N + n;
-      if (there == 8) {
-        __builtin_memcpy(&y[i], from, 16);  // at any alignment
-      } else {
-        uint16_t e[8];
+      const int m = row + 8 * i;
+      const bool want = ((wanted >> m) & 1) != 0;
+      if constexpr (kWhole) {  // (of what is not wanted, something that is there)
+        y[i] = *(const u32x4*)(p.y + (want ? min(t0 + m, p.T - 1) : t0) * p.N + (there != 0 ? n : 0));
+      } else if (want) {
+        const uint16_t* from = p.y + min(t0 + m, p.T - 1) * p.N + n;
+        if (there == 8) {
+          __builtin_memcpy(&y[i], from, 16);  // at any alignment
+        } else {
+          uint16_t e[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) e[c] = c < there ? from[c] : (uint16_t)0;
-        __builtin_memcpy(&y[i], e, 16);
+          for (int c = 0; c < 8; ++c) e[c] = c < there ? from[c] : (uint16_t)0;
+          __builtin_memcpy(&y[i], e, 16);
+        }
       }
     }
   }
@@ -320,7 +327,9 @@ struct UpRows {
       if ((none >> m) & 1) o = y[i];
       if (((write >> m) & 1) == 0 || t0 + m >= p.T) continue;
       uint16_t* out = p.out + (t0 + m) * p.N + n;
-      if (there == 8) {
+      if constexpr (kWhole) {
+        if (there != 0) *(u32x4*)out = o;
+      } else if (there == 8) {
         __builtin_memcpy(out, &o, 16);
       } else {
         uint16_t e[8];
@@ -343,9 +352,9 @@ __device__ __forceinline__ uint32_t rows_written(int adapter) {
 
 // `tiles` tiles of 16 rows, one after the other; the adapter's fragments of B stay in registers until
 // a tile has another.
-template <int kSteps, bool kHalves, int kWaves>
+template <int kSteps, bool kHalves, int kWaves, bool kWhole>
 __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int tiles) {
-  typedef UpRows<kWaves> Rows;
+  typedef UpRows<kWaves, kWhole> Rows;
   __shared__ __align__(16) float sums[2][16 * Rows::kPitch];
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -361,7 +370,6 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
     const int64_t t = t0 + 16 * j + r;
     k.adapter = adapter_of(p, t);
     k.write = gridDim.z > 1 ? rows_written(k.adapter) : 0xFFFFu;
-    if (k.write == 0) return;
     const u32x4* v = (const u32x4*)p.down + min(t, p.T - 1) * (p.R >> 2);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) k.v[i] = v[min(4 * i + q, (p.R >> 2) - 1)];
@@ -402,10 +410,10 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
 //
 // Every workgroup of 512 columns computes the v that it needs for itself, from the caches: a launch
 // less (of 3 us on the host and as much on the device) for as many readings of A.
-template <int kR, int kC, int kSteps, bool kHalves>
+template <int kR, int kC, int kSteps, bool kHalves, bool kWhole>
 __global__ void __launch_bounds__(512) lora_small_kernel(LoraProblem p) {
   constexpr int kWaves = 8, kBytes = kUnitBytes<kR, kC>;
-  typedef UpRows<kWaves> Rows;
+  typedef UpRows<kWaves, kWhole> Rows;
   static_assert(kWaves * kBytes >= 64 * Rows::kPitch && kBytes >= kR * 1024, "what follows is held in the same memory");
   __shared__ __align__(16) uint8_t lds[kWaves * kBytes];
   __shared__ __align__(16) uint16_t parts[16 * 32 * kR];
@@ -453,7 +461,9 @@ void launch_up(const LoraProblem& p, const LoraForm& f, hipStream_t stream) {
   constexpr int kWaves = 4;
   const int64_t columns = 64 * kWaves, rows = 16 * f.up_tiles;
   const dim3 grid((unsigned)((p.N + columns - 1) / columns), (unsigned)((p.T + rows - 1) / rows), (unsigned)f.up_deal);
-  hipLaunchKernelGGL((lora_up_kernel<kSteps, kHalves, kWaves>), grid, dim3(64 * kWaves), 0, stream, p, f.up_tiles);
+  const dim3 block(64 * kWaves);
+  if (p.N % 8 == 0) hipLaunchKernelGGL((lora_up_kernel<kSteps, kHalves, kWaves, true>), grid, block, 0, stream, p, f.up_tiles);
+  else hipLaunchKernelGGL((lora_up_kernel<kSteps, kHalves, kWaves, false>), grid, block, 0, stream, p, f.up_tiles);
 }
 
 template <int kR, int kC, int kWaves>
@@ -471,7 +481,8 @@ void launch_down_wide(const LoraProblem& p, hipStream_t stream) {
 template <int kR, int kC, int kSteps, bool kHalves>
 void launch_small(const LoraProblem& p, const LoraForm& f, hipStream_t stream) {
   const dim3 grid((unsigned)((p.N + 511) / 512), (unsigned)((p.T + 15) / 16), (unsigned)f.deal);
-  hipLaunchKernelGGL((lora_small_kernel<kR, kC, kSteps, kHalves>), grid, dim3(512), 0, stream, p);
+  if (p.N % 8 == 0) hipLaunchKernelGGL((lora_small_kernel<kR, kC, kSteps, kHalves, true>), grid, dim3(512), 0, stream, p);
+  else hipLaunchKernelGGL((lora_small_kernel<kR, kC, kSteps, kHalves, false>), grid, dim3(512), 0, stream, p);
 }
 
 }  // namespace

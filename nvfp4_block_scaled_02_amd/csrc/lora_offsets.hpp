@@ -35,6 +35,17 @@ NVFP4_HD int64_t lora_neighbour(int64_t i, int64_t n) {
   return xcd * each + (xcd < more ? xcd : more) + i / 8;
 }
 
+// What a launch takes, by sizes alone (how many adapters the rows have is not known).
+//
+// The first product in the second's kernel: up to 32 ranks, where repeating it for every 512 columns costs
+// less than a second launch (graph of 17 rows of their own adapters, K 4096, N 4096, 8.0 us against
+// 9.8; but 48 rows 16.2 against 10.8). One fragment of ranks per workgroup while that makes no more than 256 of
+// them (600 rows of rank 64 16.9 against 18.8 for two), two or, for many rows of high rank, all at once
+// above (2048 rows of rank 64 36.0, 32.8; 16384 of rank 128 140 for two, 94 for all). Tiles whose adapters are
+// dealt out, up to 1024 workgroups: 48 rows of rank 16 48.7, dealt to 16 11.9. The second product's
+// workgroups: 512, two to a compute unit, of up to 16 tiles each (8192 rows of rank 64 into 4096: 8 tiles
+// 76.9, 12 85.1, 16 74.5, 24 84.5).
+//
 // The form of the first product: within the second's kernel, with one or two fragments of 16 ranks
 // per tile of rows, or for many rows at once.
 enum class LoraDown { kFused, kNarrow, kPair, kWide };
@@ -55,7 +66,7 @@ NVFP4_HD LoraForm lora_form(int64_t T, int64_t N, int64_t K, int64_t R) {
   f.deal = f.down == LoraDown::kWide ? 1 : (int)lora_clamp(1024 / (tiles * parts), 1, most);
   const int64_t work = tiles * ((N + 255) / 256);
   f.up_deal = (int)lora_clamp(512 / work, 1, most);
-  f.up_tiles = (int)lora_clamp(work / 2048, 1, 16);
+  f.up_tiles = (int)lora_clamp((work + 511) / 512, 1, 16);
   return f;
 }
 

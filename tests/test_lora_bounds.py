@@ -37,7 +37,7 @@ def test_no_access_leaves_its_operand(tmp_path):
     ("staged", "^ (row & 15)", "^ (row & 31)"),
     ("columns", "16 * (r >> 2) + 4 * i", "16 * (r >> 2) + 3 * i"),
     ("neighbours", "(xcd < more ? xcd : more)", "xcd"),
-    ("forms", "lora_clamp(work / 2048, 1, 16)", "lora_clamp(work / 2048, 1, 1)"),
+    ("forms", "lora_clamp((work + 511) / 512, 1, 16)", "lora_clamp((work + 511) / 512, 1, 1)"),
 ])
 def test_planted_mistakes_are_found(tmp_path, family, was, planted):
     with open(os.path.join(CSRC, "lora_offsets.hpp")) as f:
