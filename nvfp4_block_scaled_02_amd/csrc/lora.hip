@@ -258,7 +258,7 @@ struct UpWeights {
     }
   }
   // sum = B v where `here` (v: the lane's chunks of both parts), else as it was
-  __device__ __forceinline__ void multiply(floatx4 (&sum)[4], const u32x4 (&v)[kSteps], bool here, int R, int q) const {
+  __device__ __forceinline__ void multiply(floatx4 (&sum)[4], const u32x4* v, bool here, int R, int q) const {
     floatx4 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -351,17 +351,24 @@ __device__ __forceinline__ uint32_t rows_written(int adapter) {
 }
 
 // `tiles` tiles of 16 rows, one after the other; the adapter's fragments of B stay in registers until
-// a tile has another.
+// a tile has another. Above 64 ranks the workgroup's waves share a tile's v in LDS, loaded two tiles ahead:
+// each for itself, v's bytes are more than those of y and out together (16384 rows into 4096, rank
+// 128: 210 us, shared 179; rank 64 with 8192 rows 77, 82).
 template <int kSteps, bool kHalves, int kWaves, bool kWhole>
 __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int tiles) {
   typedef UpRows<kWaves, kWhole> Rows;
+  constexpr bool kShared = kSteps > 4;
+  constexpr int kVChunks = 4 * kSteps, kVPitch = 16 * kVChunks + 16;  // (16 rows in distinct banks)
+  constexpr int kVLoads = kShared ? (16 * kVChunks + 64 * kWaves - 1) / (64 * kWaves) : 1;
   __shared__ __align__(16) float sums[2][16 * Rows::kPitch];
+  __shared__ __align__(16) uint8_t vs[kShared ? 2 : 1][kShared ? 16 * kVPitch : 16];
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t first = (int64_t)blockIdx.x * (64 * kWaves), n0 = first + 64 * wave;
   const int64_t t0 = (int64_t)blockIdx.y * (16 * tiles);
+  const int R4 = p.R >> 2;  // chunks of a row's v
   struct Tile {
-    u32x4 v[kSteps];
+    u32x4 v[kShared ? 1 : kSteps];
     Rows rows;
     int adapter;
     uint32_t write;
@@ -370,35 +377,75 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
     const int64_t t = t0 + 16 * j + r;
     k.adapter = adapter_of(p, t);
     k.write = gridDim.z > 1 ? rows_written(k.adapter) : 0xFFFFu;
-    const u32x4* v = (const u32x4*)p.down + min(t, p.T - 1) * (p.R >> 2);
+    if constexpr (!kShared) {
+      const u32x4* v = (const u32x4*)p.down + min(t, p.T - 1) * R4;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) k.v[i] = v[min(4 * i + q, (p.R >> 2) - 1)];
+      for (int i = 0; i < kSteps; ++i) k.v[i] = v[min(4 * i + q, R4 - 1)];
+    }
     k.rows.load(p, t0 + 16 * j, k.write);
+  };
+  // a thread's part of a tile's v (past the last rank: the last one's)
+  u32x4 part[kVLoads];
+  auto load_v = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < kVLoads; ++i) {
+      const int at = min(i * 64 * kWaves + (int)threadIdx.x, 16 * kVChunks - 1);
+      part[i] = ((const u32x4*)p.down)[min(t0 + 16 * j + at / kVChunks, p.T - 1) * R4 + min(at % kVChunks, R4 - 1)];
+    }
+  };
+  auto share_v = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < kVLoads; ++i) {
+      const int at = i * 64 * kWaves + (int)threadIdx.x;
+      if (at < 16 * kVChunks) *(u32x4*)&vs[j & 1][at / kVChunks * kVPitch + at % kVChunks * 16] = part[i];
+    }
+  };
+  auto meet = [&]() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
   };
   int held = -1;
   UpWeights<kSteps, kHalves> w;
   Tile now{{}, Rows(p, first), -1, 0u}, next{{}, Rows(p, first), -1, 0u};
   load(now, 0);
   if (tiles == 1 && now.write == 0) return;  // nothing for this one of a tile's workgroups
+  if constexpr (kShared) {
+    load_v(0);
+    share_v(0);
+    if (tiles > 1) load_v(1);
+    meet();
+  }
 #pragma unroll 1
   for (int j = 0; j < tiles; ++j) {
     if (j + 1 < tiles) load(next, j + 1);
+    if constexpr (kShared) {
+      if (j + 1 < tiles) share_v(j + 1);
+      if (j + 2 < tiles) load_v(j + 2);
+    }
     floatx4 sum[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     for_adapters(now.adapter, [&](int a) {
       if (a != held) w.load(p, a, n0, q, r);
       held = a;
-      w.multiply(sum, now.v, now.adapter == a, p.R, q);
+      if constexpr (kShared) {
+        u32x4 v[kSteps];
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) v[k] = *(const u32x4*)&vs[j & 1][r * kVPitch + 16 * (4 * k + q)];
+        w.multiply(sum, v, now.adapter == a, p.R, q);
+      } else {
+        w.multiply(sum, now.v, now.adapter == a, p.R, q);
+      }
     });
     float* s = sums[j & 1];  // (a buffer is written again behind the next tile's barrier)
     Rows::put(s, sum, wave, q, r);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    meet();
     now.rows.store(p, s, t0 + 16 * j, now.write, (uint32_t)__ballot(now.adapter < 0));
+    if constexpr (!kShared) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) now.v[i] = next.v[i];
+      for (int i = 0; i < kSteps; ++i) now.v[i] = next.v[i];
+    }
     now.rows.y[0] = next.rows.y[0];
     now.rows.y[1] = next.rows.y[1];
     now.adapter = next.adapter;
