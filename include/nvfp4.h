@@ -439,7 +439,8 @@ int nvfp4_lora(const void* y_bf16, const void* x_bf16, const void* a_bf16, const
  *   [0, groups) is not modulated: its scale and shift read as 0, and where there is a gate its h is x.
  *   rows NULL: M / groups rows each, in their order (M % groups == 0).
  *   H a multiple of 8 (MXFP4 and MXFP8: 32, NVFP4 and rowwise FP8: 16), at most 32768; eps > 0. All
- *   bf16 tensors and out 16-byte aligned, rows, scales and global_scale_device 4. Statistics in fp32.
+ *   bf16 tensors and out 16-byte aligned, rows, scales and global_scale_device 4. Statistics in fp32,
+ *   which has to hold the sum of a row's squares (values below 2^56 in any row).
  */
 enum nvfp4_norm_kind { NVFP4_NORM_RMS = 0, NVFP4_NORM_LAYER = 1 };
 enum nvfp4_norm_format {

@@ -70,7 +70,10 @@ CASES = [  # T, N, K, R, L
     (1, 1, 8, 8, 1), (1, 256, 512, 16, 3), (1, 4096, 4096, 16, 2), (2, 17, 40, 24, 2), (5, 1001, 2560, 32, 6), (15, 64, 264, 40, 4),
     (16, 65, 256, 48, 2), (17, 63, 72, 56, 20), (33, 130, 1032, 64, 3), (48, 333, 288, 72, 32), (64, 256, 512, 96, 2),
     (100, 96, 96, 104, 100), (255, 24, 136, 120, 3), (257, 100, 520, 128, 9), (300, 1024, 64, 8, 5), (1023, 72, 200, 16, 4),
-    (2000, 520, 256, 64, 7), (4100, 33, 48, 32, 2)]
+    (2000, 520, 256, 64, 7), (4100, 33, 48, 32, 2),
+    # many rows: all ranks of two tiles at once, several tiles per workgroup of the second product, v shared or not
+    (4100, 64, 136, 40, 3), (5000, 24, 4104, 72, 4), (4128, 200, 264, 128, 5), (4100, 2056, 72, 64, 5), (20000, 520, 40, 16, 6),
+    (9000, 4104, 64, 128, 3), (6001, 1023, 128, 96, 2), (3000, 4096, 520, 56, 4)]
 
 
 @pytest.mark.parametrize("how", ["each", "runs", "same"])
@@ -98,10 +101,10 @@ def test_rows_without_an_adapter(T):
     assert torch.equal(_run(y, x, empty[0], empty[1], torch.zeros_like(ad), empty[2]).view(torch.int16), y.view(torch.int16))
 
 
-@pytest.mark.parametrize("T", [4, 40, 400])
+@pytest.mark.parametrize("T", [4, 40, 400, 5000])
 def test_a_row_depends_on_its_own_adapter_and_activations_alone(T):
     """NaN and infinities in other adapters' weights, scales and other rows leave a row as it is."""
-    N, K, R, L = 200, 328, 24, 4
+    N, K, R, L = (200, 328, 24, 4) if T < 5000 else (1200, 328, 72, 4)
     y, x, a, b, scales = _inputs(T, N, K, R, L, 5)
     ad = _adapters(T, 3, "each", 2)
     ad[0], ad[1] = 0, 3
