@@ -277,10 +277,16 @@ struct UpWeights {
 
 // The sums pass through LDS, so that y is read and out written in whole pieces of 128 kWaves bytes of
 // a row (each lane with the columns that the matrix instruction gives it: 16 rows in every access,
-// 16384 x 4096 of rank 16 77 us instead of 63). A thread has 8 columns of two rows of a tile. kWhole: N
-// is a multiple of 8, and the loads have no branch around them that would wait for them.
-template <int kWaves, bool kWhole>
+// 16384 x 4096 of rank 16 77 us instead of 63). A thread has 8 columns of two rows of a tile.
+//
+// kWhole: N is a multiple of 8, and the loads have no branch around them that would wait for them.
+// kPassing: they leave the caches to v and B, as the stores do; where y is larger than these
+// (both products, 16384 x 4096 of rank 16, 91.7 us, passing 86.0; 8192 x 4096 of rank 64 73.6, 66.5; but
+// 4096 x 2048 20.5, 22.7. With stores that do not pass 96.7, 77.1 and 21.7).
+enum class Rows { kAny, kWhole, kPassing };
+template <int kWaves, Rows kRows>
 struct UpRows {
+  static constexpr bool kWhole = kRows != Rows::kAny;
   static constexpr int kPitch = 64 * kWaves + 4;  // floats
   const int row, column;
   const int64_t n;
@@ -295,7 +301,8 @@ struct UpRows {
       const int m = row + 8 * i;
       const bool want = ((wanted >> m) & 1) != 0;
       if constexpr (kWhole) {  // (of what is not wanted, something that is there)
-        y[i] = *(const u32x4*)(p.y + (want ? min(t0 + m, p.T - 1) : t0) * p.N + (there != 0 ? n : 0));
+        const u32x4* from = (const u32x4*)(p.y + (want ? min(t0 + m, p.T - 1) : t0) * p.N + (there != 0 ? n : 0));
+        y[i] = kRows == Rows::kPassing ? __builtin_nontemporal_load(from) : *from;
       } else if (want) {
         const uint16_t* from = p.y + min(t0 + m, p.T - 1) * p.N + n;
         if (there == 8) {
@@ -328,7 +335,7 @@ struct UpRows {
       if (((write >> m) & 1) == 0 || t0 + m >= p.T) continue;
       uint16_t* out = p.out + (t0 + m) * p.N + n;
       if constexpr (kWhole) {
-        if (there != 0) *(u32x4*)out = o;
+        if (there != 0) __builtin_nontemporal_store(o, (u32x4*)out);
       } else if (there == 8) {
         __builtin_memcpy(out, &o, 16);
       } else {
@@ -354,13 +361,13 @@ __device__ __forceinline__ uint32_t rows_written(int adapter) {
 // a tile has another. Above 64 ranks the workgroup's waves share a tile's v in LDS, loaded two tiles ahead:
 // each for itself, v's bytes are more than those of y and out together (16384 rows into 4096, rank
 // 128: 210 us, shared 179; rank 64 with 8192 rows 77, 82).
-template <int kSteps, bool kHalves, int kWaves, bool kWhole>
+template <int kSteps, bool kHalves, int kWaves, Rows kRows>
 __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int tiles) {
-  typedef UpRows<kWaves, kWhole> Rows;
+  typedef UpRows<kWaves, kRows> Part;
   constexpr bool kShared = kSteps > 4;
   constexpr int kVChunks = 4 * kSteps, kVPitch = 16 * kVChunks + 16;  // (16 rows in distinct banks)
   constexpr int kVLoads = kShared ? (16 * kVChunks + 64 * kWaves - 1) / (64 * kWaves) : 1;
-  __shared__ __align__(16) float sums[2][16 * Rows::kPitch];
+  __shared__ __align__(16) float sums[2][16 * Part::kPitch];
   __shared__ __align__(16) uint8_t vs[kShared ? 2 : 1][kShared ? 16 * kVPitch : 16];
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
   const int R4 = p.R >> 2;  // chunks of a row's v
   struct Tile {
     u32x4 v[kShared ? 1 : kSteps];
-    Rows rows;
+    Part rows;
     int adapter;
     uint32_t write;
   };
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
   };
   int held = -1;
   UpWeights<kSteps, kHalves> w;
-  Tile now{{}, Rows(p, first), -1, 0u}, next{{}, Rows(p, first), -1, 0u};
+  Tile now{{}, Part(p, first), -1, 0u}, next{{}, Part(p, first), -1, 0u};
   load(now, 0);
   if (tiles == 1 && now.write == 0) return;  // nothing for this one of a tile's workgroups
   if constexpr (kShared) {
@@ -439,7 +446,7 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
       }
     });
     float* s = sums[j & 1];  // (a buffer is written again behind the next tile's barrier)
-    Rows::put(s, sum, wave, q, r);
+    Part::put(s, sum, wave, q, r);
     meet();
     now.rows.store(p, s, t0 + 16 * j, now.write, (uint32_t)__ballot(now.adapter < 0));
     if constexpr (!kShared) {
@@ -457,11 +464,11 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
 //
 // Every workgroup of 512 columns computes the v that it needs for itself, from the caches: a launch
 // less (of 3 us on the host and as much on the device) for as many readings of A.
-template <int kR, int kC, int kSteps, bool kHalves, bool kWhole>
+template <int kR, int kC, int kSteps, bool kHalves, Rows kRows>
 __global__ void __launch_bounds__(512) lora_small_kernel(LoraProblem p) {
   constexpr int kWaves = 8, kBytes = kUnitBytes<kR, kC>;
-  typedef UpRows<kWaves, kWhole> Rows;
-  static_assert(kWaves * kBytes >= 64 * Rows::kPitch && kBytes >= kR * 1024, "what follows is held in the same memory");
+  typedef UpRows<kWaves, kRows> Part;
+  static_assert(kWaves * kBytes >= 64 * Part::kPitch && kBytes >= kR * 1024, "what follows is held in the same memory");
   __shared__ __align__(16) uint8_t lds[kWaves * kBytes];
   __shared__ __align__(16) uint16_t parts[16 * 32 * kR];
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(512) lora_small_kernel(LoraProblem p) {
   const int adapter = adapter_of(p, t0 + r);
   const uint32_t write = rows_written(adapter);
   if (write == 0) return;  // nothing for this one of a tile's workgroups
-  Rows rows(p, first);
+  Part rows(p, first);
   rows.load(p, t0, write);
   floatx4 sum[4];
 #pragma unroll
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(512) lora_small_kernel(LoraProblem p) {
     w.multiply(sum, v, adapter == a, p.R, q);
   });
   __syncthreads();
-  Rows::put((float*)lds, sum, wave, q, r);
+  Part::put((float*)lds, sum, wave, q, r);
   __syncthreads();
   rows.store(p, (const float*)lds, t0, write, (uint32_t)__ballot(adapter < 0));
 }
@@ -509,8 +516,9 @@ void launch_up(const LoraProblem& p, const LoraForm& f, hipStream_t stream) {
   const int64_t columns = 64 * kWaves, rows = 16 * f.up_tiles;
   const dim3 grid((unsigned)((p.N + columns - 1) / columns), (unsigned)((p.T + rows - 1) / rows), (unsigned)f.up_deal);
   const dim3 block(64 * kWaves);
-  if (p.N % 8 == 0) hipLaunchKernelGGL((lora_up_kernel<kSteps, kHalves, kWaves, true>), grid, block, 0, stream, p, f.up_tiles);
-  else hipLaunchKernelGGL((lora_up_kernel<kSteps, kHalves, kWaves, false>), grid, block, 0, stream, p, f.up_tiles);
+  if (p.N % 8 != 0) hipLaunchKernelGGL((lora_up_kernel<kSteps, kHalves, kWaves, Rows::kAny>), grid, block, 0, stream, p, f.up_tiles);
+  else if (f.passing) hipLaunchKernelGGL((lora_up_kernel<kSteps, kHalves, kWaves, Rows::kPassing>), grid, block, 0, stream, p, f.up_tiles);
+  else hipLaunchKernelGGL((lora_up_kernel<kSteps, kHalves, kWaves, Rows::kWhole>), grid, block, 0, stream, p, f.up_tiles);
 }
 
 template <int kR, int kC, int kWaves>
@@ -528,8 +536,8 @@ void launch_down_wide(const LoraProblem& p, hipStream_t stream) {
 template <int kR, int kC, int kSteps, bool kHalves>
 void launch_small(const LoraProblem& p, const LoraForm& f, hipStream_t stream) {
   const dim3 grid((unsigned)((p.N + 511) / 512), (unsigned)((p.T + 15) / 16), (unsigned)f.deal);
-  if (p.N % 8 == 0) hipLaunchKernelGGL((lora_small_kernel<kR, kC, kSteps, kHalves, true>), grid, dim3(512), 0, stream, p);
-  else hipLaunchKernelGGL((lora_small_kernel<kR, kC, kSteps, kHalves, false>), grid, dim3(512), 0, stream, p);
+  if (p.N % 8 == 0) hipLaunchKernelGGL((lora_small_kernel<kR, kC, kSteps, kHalves, Rows::kWhole>), grid, dim3(512), 0, stream, p);
+  else hipLaunchKernelGGL((lora_small_kernel<kR, kC, kSteps, kHalves, Rows::kAny>), grid, dim3(512), 0, stream, p);
 }
 
 }  // namespace

@@ -54,19 +54,21 @@ struct LoraForm {
   int deal;      // its workgroups that share the distinct adapters of a tile of 16 rows
   int up_deal;   // the second product's
   int up_tiles;  // tiles of 16 rows per workgroup of the second product
+  bool passing;  // whether its y and out leave the caches alone (32 MB of y on)
 };
 NVFP4_HD int64_t lora_clamp(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 NVFP4_HD LoraForm lora_form(int64_t T, int64_t N, int64_t K, int64_t R) {
   const int64_t tiles = (T + 15) / 16, slices = (N + 511) / 512, parts = (R + 15) / 16, most = T < 16 ? T : 16;
   LoraForm f;
-  if (tiles < 1 || slices < 1) return LoraForm{LoraDown::kFused, 1, 1, 1};
+  if (tiles < 1 || slices < 1) return LoraForm{LoraDown::kFused, 1, 1, 1, false};
   if (R <= 32 && (tiles * slices <= 16 || (slices == 1 && tiles <= 64)))
-    return LoraForm{LoraDown::kFused, (int)lora_clamp(256 / (tiles * slices), 1, most), 1, 1};
+    return LoraForm{LoraDown::kFused, (int)lora_clamp(256 / (tiles * slices), 1, most), 1, 1, false};
   f.down = R <= 16 || tiles * parts <= 256 ? LoraDown::kNarrow : R <= 32 || T <= 4096 ? LoraDown::kPair : LoraDown::kWide;
   f.deal = f.down == LoraDown::kWide ? 1 : (int)lora_clamp(1024 / (tiles * parts), 1, most);
   const int64_t work = tiles * ((N + 255) / 256);
   f.up_deal = (int)lora_clamp(512 / work, 1, most);
   f.up_tiles = (int)lora_clamp((work + 511) / 512, 1, 16);
+  f.passing = T * N >= (int64_t)1 << 24;
   return f;
 }
 
