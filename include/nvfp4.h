@@ -388,8 +388,9 @@ int nvfp4_mxfp4_moe_routed(const void* x_bf16, const void* topk_ids, const void*
  *   (NVFP4_MOE_SIGMOID); key_e = score_e + bias_e (bias fp32 [E], or NULL).
  *   Of `groups` groups of E / groups consecutive experts the top_groups of largest score stay; a
  *   group's score is the sum of its group_best (1 or 2) largest keys, of those it has. Of
- *   their experts the top_k of largest key are chosen, in falling order (without a bias: of
- *   largest logit). Ties go to the lowest index. Keys and sums are held in 64 bits.
+ *   their experts the top_k of largest key are chosen, in falling order. Without a bias the order
+ *   is that of the logits, of groups too if group_best is 1. Ties go to the lowest index. Keys
+ *   and sums are those of 64 bits.
  *   weight = scale * score, divided by the sum of the chosen scores if renormalize == 1.
  *   A logit or key of -inf is never chosen; where nothing is left to choose the id is -1 and the
  *   weight 0 (a row of -inf marks padding). A NaN key ranks first. A NaN logit makes its weight NaN,

@@ -6,15 +6,16 @@
 // An expert whose logit or key is -inf is never chosen; a NaN key comes first. Of G groups of E / G
 // consecutive experts the top_groups of largest score stay, a group's score being the sum of its
 // group_best (1 or 2) largest keys, of those that it has. Of their experts the top_k of largest
-// key are chosen, in falling order; without a bias the order is that of the logits. Ties go to the
-// lowest index. weight = scale * score, over the chosen experts' sum if renormalized.
+// key are chosen, in falling order. Without a bias the order is that of the logits, of groups too if
+// their largest alone counts. Ties go to the lowest index. weight = scale * score, over the chosen experts' sum if renormalized.
 //
 // Keys and sums are defined in 64 bits: what is next to each other in rank is told apart as the formula
 // has it, where 32 bits would order by their own rounding. Computing them so for all experts is
 // bound by the 64-bit exponentials and the selection of 64-bit keys (32768 x 256, 73 us for 36 MB). So
-// 16 lanes choose for a token by 32-bit keys (route_rows), and know when these do not tell: two keys
-// next to each other closer than their error bound. Such a token, about one in a hundred,
-// is chosen again by a whole wave in 64 bits (route_exact).
+// 16 lanes choose for a token by 32-bit keys (route_rows; 23 us), and know when these do not tell: two
+// keys next to each other closer than their error bound. Those few are compared as the formula has
+// them; what that leaves, some tokens in ten thousand, a whole wave chooses again in 64 bits
+// (route_exact).
 #include "kernels.hpp"
 #include "wave.hpp"
 
@@ -113,6 +114,12 @@ __device__ __forceinline__ void route_exact(const RouteProblem& p, int64_t t, in
     if (p.bias && e < p.E) k += (double)p.bias[e];
     key[i] = l[i] == -__builtin_inff() ? 0ull : order_of(k);
   }
+  auto by_logit = [&]() {  // the order of the logits: shares of different logits can round to the same
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (key[i] != 0ull) key[i] = order_of((double)l[i]);
+  };
+  if (!p.bias && p.group_best == 1) by_logit();
   if (p.top_groups < p.groups) {
     // a group per lane
     const int size = p.E / p.groups;
@@ -148,11 +155,7 @@ __device__ __forceinline__ void route_exact(const RouteProblem& p, int64_t t, in
       if (g >= 64 || !((open >> g) & 1)) key[i] = 0ull;
     }
   }
-  if (!p.bias) {  // the order of the logits: shares of different logits can round to the same
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (key[i] != 0ull) key[i] = order_of((double)l[i]);
-  }
+  if (!p.bias && p.group_best == 2) by_logit();
   // lane j: the j-th choice
   int id = -1;
   float chosen = 0.0f;
@@ -249,10 +252,12 @@ struct Key32 {
 // below kPer 2^-22 of its value together (cut; before it, for the groups, 2^-22). A sigmoid s: its
 // exponential's argument is off by at most 2.2 * 2^-24 of itself, which moves s by that times
 // |l| s (1 - s) < 0.23; the hardware's exponential and reciprocal, a last place each (2^-23), move
-// it by s (1 - s) 2^-23 and s 2^-23, the sum between them by s 2^-24: below 2^-22 in all. A share p of a softmax with largest share m: likewise |l - top| exp(l - top) < 0.37, below 2^-21 m; all
-// shares of a row by the same factor, their sum's, within 2^-19. So two keys tell their order if
-// they are further apart than cut + 2^-21, or cut + 2^-18 m; without a bias, where shares may be
-// small, a score is good to 2^-18 of itself (arguments up to 40) and is not trusted below 2^-40 m.
+// it by s (1 - s) 2^-23 and s 2^-23, the sum between them by s 2^-24: below 2^-22 in all. A share p
+// of a softmax with largest share m: likewise |l - top| exp(l - top) < 0.37, below 2^-21 m; all
+// shares of a row by the same factor, their sum's (36 additions on the way), within 2^-18. So two
+// keys tell their order if they are further apart than cut + 2^-21, or cut + 2^-17 m. Without a
+// bias, where shares may be small, a score is good to 2^-16.8 of itself (arguments up to 68), two
+// are told apart by 2^-15, and none is trusted below 2^-40 m.
 template <int kPer, bool kScored, bool kSigmoid>
 __global__ void __launch_bounds__(256) route_rows_kernel(RouteProblem p, int per, bool whole) {
   constexpr uint32_t kPlace = kPer - 1;
@@ -326,8 +331,8 @@ __global__ void __launch_bounds__(256) route_rows_kernel(RouteProblem p, int per
   // whether a and b, sums of n keys off by `cut` of their value each, may be in another order than theirs
   auto near = [&](float a, float b, float n, float cut) {
     cut *= __builtin_fmaxf(__builtin_fabsf(a), __builtin_fabsf(b));
-    if (p.bias) return !(__builtin_fabsf(a - b) > n * (cut + (kSigmoid ? 0x1p-21f : 0x1p-18f * most)));
-    return !(__builtin_fabsf(a - b) > n * (cut + 0x1p-16f * a)) || a < 0x1p-40f * most;
+    if (p.bias) return !(__builtin_fabsf(a - b) > n * (cut + (kSigmoid ? 0x1p-21f : 0x1p-17f * most)));
+    return !(__builtin_fabsf(a - b) > n * (cut + 0x1p-15f * a)) || a < 0x1p-40f * most;
   };
   bool open = true;  // this lane's group
   if (p.top_groups < p.groups) {
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(RouteProblem p, int per
     open = before < p.top_groups;
     // the worst that stays against the best that does not
     const float in = -row_maxf(open ? -score : -__builtin_inff()), out = row_maxf(open ? -__builtin_inff() : score);
-    if (out > -__builtin_inff()) unsure = unsure || (kScored ? near(in, out, 2.0f, 0x1p-22f) : in == out);
+    if (kScored && out > -__builtin_inff()) unsure = unsure || near(in, out, 2.0f, 0x1p-22f);
   }
   // v = before - 1 - key of each round; a lane whose group is out has nothing
 #pragma unroll

@@ -44,7 +44,10 @@ def route(logits, top_k, bias=None, scores="softmax", groups=1, top_groups=None,
             of = {}
             for g in range(groups):
                 mine = sorted((e for e in there if e // size == g), key=rank(key))
-                if mine:
+                if mine and bias is None and group_best == 1:  # their largest alone: the order of the logits
+                    of[g] = max((l[e] for e in mine if not math.isnan(l[e])), default=math.nan)
+                    of[g] = math.nan if any(math.isnan(l[e]) for e in mine) else of[g]
+                elif mine:
                     of[g] = sum(key[e] for e in mine[:group_best])
             kept = sorted(of, key=rank(of))[:keep]
             there = [e for e in there if e // size in kept]

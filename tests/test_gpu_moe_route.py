@@ -53,11 +53,11 @@ def test_route(shape, scores):
                        renormalize=renormalize, scale=2.5 if b is None else 1.0)
 
 
-@pytest.mark.parametrize("E,groups,top", [(12, 1, 1), (12, 4, 2), (96, 3, 2), (320, 32, 3)])
+@pytest.mark.parametrize("E,groups,top", [(12, 1, 1), (12, 4, 2), (96, 3, 2), (320, 32, 3), (64, 4, 2), (160, 8, 3), (512, 16, 5), (48, 2, 1)])
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
 def test_masked_and_unordered(E, groups, top, scores):
     k, low = 4, torch.finfo(torch.float32).min
-    l = _logits(14, E, E)
+    l = _logits(18, E, E)
     l[0] = -INF                      # padding
     l[1, 1:] = -INF                  # one expert
     l[2] = low                       # the type's lowest value is a value like any other
@@ -72,6 +72,11 @@ def test_masked_and_unordered(E, groups, top, scores):
     l[11], l[11, 3] = 0.0, -0.0
     l[12] = 100.0 + torch.arange(E, device="cuda") % 5  # sigmoids that are all 1
     l[13, 2:] = -INF
+    l[14] = 60.0 + 30.0 * torch.arange(E, device="cuda") / E   # the same, in rising order
+    l[15] = -800.0 - torch.arange(E, device="cuda").flip(0)    # far from the first one
+    l[15, 0] = 0.0
+    l[16] = -45.0 - torch.arange(E, device="cuda") % 7
+    l[17] = torch.arange(E, device="cuda") % 3 - 30.0
     bias = torch.linspace(0.2, -0.2, E, device="cuda")
     off = bias.clone()
     off[::3] = -INF                  # experts that are switched off
