@@ -66,7 +66,7 @@ __device__ __forceinline__ void two_parts(const floatx4 v, u32x2& hi, u32x2& lo)
 // A workgroup's waves take units of 8 kC elements of K in turn, each for itself. A unit comes through
 // LDS (16 kC consecutive bytes of a row, 64 / kC rows per load): loaded in the matrix instruction's
 // order, every load touches 16 rows (16384 rows of K 4096 and rank 16 57 us instead of 37, 1999 of
-// rank 64 52 instead of 26). Chunk c (16 bytes) of row s sits at slot c ^ (s % 16), so that the
+// rank 64 52 instead of 26, both before the parts of a tile's ranks were neighbours). Chunk c (16 bytes) of row s sits at slot c ^ (s % 16), so that the
 // 16 rows of a fragment read are in distinct banks.
 template <int kR, int kC>
 constexpr int kUnitBytes = (1 + kR) * 16 * 16 * kC;
@@ -131,8 +131,9 @@ __global__ void __launch_bounds__(64 * kWaves) lora_down_kernel(LoraProblem p) {
   __shared__ __align__(16) uint8_t lds[kWaves * kBytes];
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = lora_neighbour(blockIdx.x, gridDim.x) * 16;
-  const int r0 = 16 * kR * (int)blockIdx.y;
+  const LoraPart part_of = lora_part(blockIdx.x, gridDim.x, p.R, 16 * kR);
+  const int64_t t0 = part_of.tile * 16;
+  const int r0 = part_of.rank;
   const int adapter = lane < 16 ? adapter_of(p, t0 + lane) : -1;
   const __amdgpu_buffer_rsrc_t rx = x_window(p, t0, 16);
   for_adapters(adapter, [&](int a) {
@@ -168,8 +169,9 @@ __global__ void __launch_bounds__(64 * kTok * kSplit) lora_down_wide_kernel(Lora
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tile = wave % kTok, split = wave / kTok;
-  const int64_t t0 = lora_neighbour(blockIdx.x, gridDim.x) * (16 * kTok);
-  const int r0 = 16 * kR * (int)blockIdx.y;
+  const LoraPart part_of = lora_part(blockIdx.x, gridDim.x, p.R, 16 * kR);
+  const int64_t t0 = part_of.tile * (16 * kTok);
+  const int r0 = part_of.rank;
   const int adapter = lane < 16 * kTok ? adapter_of(p, t0 + lane) : -1;
   const int chunks = (int)(p.K >> 3), stages = (chunks + kC - 1) / kC;
   const uint32_t pitch = (uint32_t)(p.K * 2);
@@ -523,13 +525,13 @@ void launch_up(const LoraProblem& p, const LoraForm& f, hipStream_t stream) {
 
 template <int kR, int kC, int kWaves>
 void launch_down(const LoraProblem& p, const LoraForm& f, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.T + 15) / 16), (unsigned)((p.R + 16 * kR - 1) / (16 * kR)), (unsigned)f.deal);
+  const dim3 grid((unsigned)((p.T + 15) / 16 * ((p.R + 16 * kR - 1) / (16 * kR))), 1, (unsigned)f.deal);
   hipLaunchKernelGGL((lora_down_kernel<kR, kC, kWaves>), grid, dim3(64 * kWaves), 0, stream, p);
 }
 
 template <int kR, int kTok, int kSplit, int kC, int kBufs>
 void launch_down_wide(const LoraProblem& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.T + 16 * kTok - 1) / (16 * kTok)), (unsigned)((p.R + 16 * kR - 1) / (16 * kR)));
+  const dim3 grid((unsigned)((p.T + 16 * kTok - 1) / (16 * kTok) * ((p.R + 16 * kR - 1) / (16 * kR))));
   hipLaunchKernelGGL((lora_down_wide_kernel<kR, kTok, kSplit, kC, kBufs>), grid, dim3(64 * kTok * kSplit), 0, stream, p);
 }
 

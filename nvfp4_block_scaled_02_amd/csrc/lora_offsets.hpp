@@ -35,13 +35,25 @@ NVFP4_HD int64_t lora_neighbour(int64_t i, int64_t n) {
   return xcd * each + (xcd < more ? xcd : more) + i / 8;
 }
 
+// The first product's workgroup i of n: its tile of rows and its first rank, `ranks` of them. The parts of a
+// tile's ranks are neighbours, so that x comes from memory for one of them.
+struct LoraPart {
+  int64_t tile;
+  int rank;
+};
+NVFP4_HD LoraPart lora_part(uint32_t i, uint32_t n, int R, int ranks) {
+  const uint32_t parts = (uint32_t)((R + ranks - 1) / ranks), at = (uint32_t)lora_neighbour(i, n);
+  return LoraPart{(int64_t)(at / parts), (int)(at % parts) * ranks};
+}
+
 // What a launch takes, by sizes alone (how many adapters the rows have is not known).
 //
 // The first product in the second's kernel: up to 32 ranks, where repeating it for every 512 columns costs
 // less than a second launch (graph of 17 rows of their own adapters, K 4096, N 4096, 8.0 us against
-// 9.8; but 48 rows 16.2 against 10.8). One fragment of ranks per workgroup while that makes no more than 256 of
-// them (600 rows of rank 64 16.9 against 18.8 for two), two or, for many rows of high rank, all at once
-// above (2048 rows of rank 64 36.0, 32.8; 16384 of rank 128 140 for two, 94 for all). Tiles whose adapters are
+// 9.8; but 48 rows 16.2 against 10.8). One fragment of ranks per workgroup up to 48 ranks (2000 rows of
+// rank 48 14.6 against 17.1 for two) and where that makes no more than 128 workgroups (450 rows of rank
+// 64 12.1, 12.5; 600 13.5, 12.3); two above, or for many rows all at once (1999 rows of rank 64 20.1,
+// 18.9, 38.5 for all; 8192 36.7, 35.3, 34.1; 16384 of rank 128 131, 128, 85). Tiles whose adapters are
 // dealt out, up to 1024 workgroups: 48 rows of rank 16 48.7, dealt to 16 11.9. The second product's
 // workgroups: 512, two to a compute unit, of up to 16 tiles each (8192 rows of rank 64 into 4096: 8 tiles
 // 76.9, 12 85.1, 16 74.5, 24 84.5).
@@ -63,7 +75,7 @@ NVFP4_HD LoraForm lora_form(int64_t T, int64_t N, int64_t K, int64_t R) {
   if (tiles < 1 || slices < 1) return LoraForm{LoraDown::kFused, 1, 1, 1, false};
   if (R <= 32 && (tiles * slices <= 16 || (slices == 1 && tiles <= 64)))
     return LoraForm{LoraDown::kFused, (int)lora_clamp(256 / (tiles * slices), 1, most), 1, 1, false};
-  f.down = R <= 16 || tiles * parts <= 256 ? LoraDown::kNarrow : R <= 32 || T <= 4096 ? LoraDown::kPair : LoraDown::kWide;
+  f.down = R <= 48 || tiles * parts <= 128 ? LoraDown::kNarrow : T <= 4096 ? LoraDown::kPair : LoraDown::kWide;
   f.deal = f.down == LoraDown::kWide ? 1 : (int)lora_clamp(1024 / (tiles * parts), 1, most);
   const int64_t work = tiles * ((N + 255) / 256);
   f.up_deal = (int)lora_clamp(512 / work, 1, most);

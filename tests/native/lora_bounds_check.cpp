@@ -81,6 +81,19 @@ int main() {
     }
     for (int64_t i = 0; i < n; ++i) expect(at[i] == 1, "once", i, n, at[i]);
   }
+  // the first product's workgroups: every part of every tile once
+  for (int tiles : {1, 2, 7, 8, 125, 4099})
+    for (int R : {8, 16, 24, 64, 120, 128})
+      for (int ranks : {16, 32, 64}) {
+        const int parts = (R + ranks - 1) / ranks;
+        std::vector<int> seen((size_t)tiles * parts, 0);
+        for (int i = 0; i < tiles * parts; ++i) {
+          const LoraPart at = lora_part((uint32_t)i, (uint32_t)(tiles * parts), R, ranks);
+          expect(at.tile >= 0 && at.tile < tiles && at.rank >= 0 && at.rank < R && at.rank % ranks == 0, "part", i, at.tile, at.rank);
+          if (at.tile >= 0 && at.tile < tiles && at.rank >= 0 && at.rank < R) ++seen[(size_t)at.tile * parts + at.rank / ranks];
+        }
+        for (size_t i = 0; i < seen.size(); ++i) expect(seen[i] == 1, "part once", (long long)i, R, ranks);
+      }
   family("neighbours");
 
   for (int64_t T : {1, 2, 15, 16, 17, 48, 255, 256, 257, 1000, 1024, 1025, 4096, 4097, 65536, 1 << 20, 1 << 21})
