@@ -407,9 +407,9 @@ int nvfp4_moe_route(const void* logits, const void* bias, int64_t T, int64_t E, 
 /*
  * nvfp4_lora: the low-rank adapters of many requests beside a shared projection.
  *   out[t] = bf16_RNE(y[t] + scales[a] * B[a] (A[a] x[t])), a = adapters[t]; a row whose adapter is
- *   outside [0, L) has none: out[t] = y[t]. Rows come in any order. Sums in fp32; A[a] x[t] is held
- *   to 2^-16 of its value for the second product (in two parts: an infinite value of B[a] gives NaN
- *   where the formula may have an infinity). A row depends on its own adapter alone.
+ *   outside [0, L) has none: out[t] = y[t]. Rows come in any order. Sums in fp32, in which A[a] x[t] is
+ *   held for the second product too (in three parts: an infinite value of B[a] gives NaN where the
+ *   formula may have an infinity). A row depends on its own adapter alone.
  *   y_bf16 [T, N] (the projection's output), x_bf16 [T, K], a_bf16 [L, R, K], b_bf16 [L, N, R],
  *   adapters int32 [T], scales fp32 [L] (NULL: 1), out_bf16 [T, N], which may be y. Adapters of
  *   smaller rank are padded with zeros.

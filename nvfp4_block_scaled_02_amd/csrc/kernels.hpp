@@ -214,7 +214,7 @@ struct LoraProblem {
   const int* adapters;  // [T]; outside [0, L): none
   const float* scales;  // [L], or null: 1
   uint16_t* out;        // bf16 [T, N]; may be y
-  uint16_t* down;       // lora_down_bytes(T, N, K, R): A x, two bf16 parts
+  uint16_t* down;       // lora_down_bytes(T, N, K, R): A x, three bf16 parts
   int64_t T, N, K, L;
   int R;
 };

@@ -11,9 +11,11 @@
 // the columns whose adapter it is. Where there are few rows the adapters are dealt out to several
 // workgroups (grid z) instead.
 //
-// Between the kernels v is held in two bf16 parts that add up to it within 2^-16 of its value: the
-// matrix instruction takes bf16, and rounded to it once v would be off by as much as the
-// output's own rounding.
+// Between the products v keeps its 32 bits: the matrix instruction takes bf16, so v goes in as three
+// bf16 parts that add up to it. (Two, 2^-16 of it, turn the rounding of 3 outputs in a thousand from
+// what fp32 gives, three of 2 in ten thousand, as any other order of the sums does; the third takes
+// 0 to 3 % of both products' time: 1999 rows of rank 64 into 14336 54.6 us instead of 53.0, 16384 rows of
+// rank 16 into 4096 86.1 instead of 84.9.)
 #include "gemm_common.hpp"
 #include "lora_offsets.hpp"
 
@@ -47,18 +49,25 @@ __device__ __forceinline__ void for_adapters(int adapter, const F& f) {
   }
 }
 
-// A value in two bf16 parts: the upper half of its 32 bits (cut, so that it overflows with the
-// value alone), and the rest, rounded. An infinity has no rest.
-__device__ __forceinline__ void two_parts(const floatx4 v, u32x2& hi, u32x2& lo) {
+// Four values in three bf16 parts each: 8 bits of a value (cut, so that they overflow with the value
+// alone), 8 of the rest, and what is left, which has 8 at most: their sum is the value itself (below
+// 2^-109, where bits of the last part are below the least bf16, within 2^-134). An infinity has no rest.
+struct Parts {
+  u32x2 of[3];
+};
+__device__ __forceinline__ Parts three_parts(const floatx4 v) {
   float rest[4];
-  uint32_t b[4];
+  uint32_t b[4], m[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     b[j] = f2u(v[j]);
     rest[j] = (b[j] & 0x7FFFFFFFu) == 0x7F800000u ? 0.0f : v[j] - u2f(b[j] & 0xFFFF0000u);
+    m[j] = f2u(rest[j]);
+    rest[j] -= u2f(m[j] & 0xFFFF0000u);
   }
-  hi = u32x2{(b[0] >> 16) | (b[1] & 0xFFFF0000u), (b[2] >> 16) | (b[3] & 0xFFFF0000u)};
-  lo = bf16x4_rne(rest[0], rest[1], rest[2], rest[3]);
+  return Parts{{u32x2{(b[0] >> 16) | (b[1] & 0xFFFF0000u), (b[2] >> 16) | (b[3] & 0xFFFF0000u)},
+                u32x2{(m[0] >> 16) | (m[1] & 0xFFFF0000u), (m[2] >> 16) | (m[3] & 0xFFFF0000u)},
+                bf16x4_rne(rest[0], rest[1], rest[2], rest[3])}};
 }
 
 // ---- v = s A x, 16 rows ----
@@ -116,12 +125,21 @@ __device__ __forceinline__ floatx4 down_sum(const floatx4* part, int i, int lane
   for (int n = 1; n < kWaves; ++n) v += part[(n * kR + i) * 64 + lane];
   return v;
 }
-// Four ranks of a row's v, scaled, in its two parts: [upper R, lower R].
-__device__ __forceinline__ void store_parts(uint16_t* row, int rank, int R, const floatx4 v) {
-  u32x2 hi, lo;
-  two_parts(v, hi, lo);
-  *(u32x2*)&row[rank] = hi;
-  *(u32x2*)&row[R + rank] = lo;
+// Four ranks of row r's v, scaled, in its parts: to chunks of a tile (lora_chunk), as the second product
+// loads them: a chunk's 16 rows together, so that 64 lanes load 1024 consecutive bytes (row by row each
+// lane would meet a line of its own: 8192 rows of rank 64 into 4096 45 us instead of 39).
+__device__ __forceinline__ void store_parts(u32x4* tile, int r, int rank, int R, const floatx4 v) {
+  const Parts parts = three_parts(v);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) ((u32x2*)&tile[(i * (R >> 3) + (rank >> 3)) * 16 + r])[(rank >> 2) & 1] = parts.of[i];
+}
+// Of a tile, the chunk that a lane takes in step k (where it has none: the first).
+__device__ __forceinline__ u32x4 v_chunk(const u32x4* tile, int k, int steps, int R, int q, int r) {
+  return tile[max(lora_chunk(k, q, steps, R), 0) * 16 + r];
+}
+// The chunks of a tile of 16 rows in the workspace.
+__device__ __forceinline__ u32x4* v_tile(const LoraProblem& p, int64_t tile) {
+  return (u32x4*)p.down + tile * lora_tile_chunks(p.R);
 }
 
 template <int kR, int kC, int kWaves>
@@ -149,7 +167,7 @@ __global__ void __launch_bounds__(64 * kWaves) lora_down_kernel(LoraProblem p) {
     for (int i = wave; i < kR; i += kWaves) {
       const int rank = r0 + 16 * i + 4 * q;  // R % 8 == 0: four ranks are all there or none
       if (__shfl(adapter, r, 64) == a && rank < p.R)
-        store_parts(p.down + (t0 + r) * (2 * p.R), rank, p.R, down_sum<kR, kWaves>(part, i, lane) * s);
+        store_parts(v_tile(p, part_of.tile), r, rank, p.R, down_sum<kR, kWaves>(part, i, lane) * s);
     }
     __syncthreads();
   });
@@ -216,7 +234,7 @@ __global__ void __launch_bounds__(64 * kTok * kSplit) lora_down_wide_kernel(Lora
     const bool here = __shfl(adapter, 16 * tile + r, 64) == a;
     auto store = [&](int i, const floatx4 v) {
       const int rank = r0 + 16 * i + 4 * q;
-      if (here && rank < p.R) store_parts(p.down + (t0 + 16 * tile + r) * (2 * p.R), rank, p.R, v * s);
+      if (here && rank < p.R) store_parts(v_tile(p, part_of.tile * kTok + tile), r, rank, p.R, v * s);
     };
     if constexpr (kSplit == 1) {
 #pragma unroll
@@ -240,10 +258,11 @@ __global__ void __launch_bounds__(64 * kTok * kSplit) lora_down_wide_kernel(Lora
 // ---- out = y + B v ----
 //
 // 64 columns of the output per wave, as four fragments of 16 rows of B such that a lane's results are
-// 16 consecutive columns of its row. kSteps: lora_steps, kHalves: lora_halves.
+// 16 consecutive columns of its row. kSteps: lora_steps, kHalves: lora_halves. The lower parts, kLast
+// steps, multiply the fragments of the first steps again.
 template <int kSteps, bool kHalves>
 struct UpWeights {
-  static constexpr int kW = kHalves ? kSteps / 2 : kSteps;
+  static constexpr int kW = kHalves ? kSteps / 2 : kSteps, kLast = (kSteps + 1) / 2, kAll = kSteps + kLast;
   u32x4 w[kW][4];
   __device__ __forceinline__ void load(const LoraProblem& p, int a, int64_t n0, int q, int r) {
     const int R8 = p.R >> 3;
@@ -259,16 +278,17 @@ struct UpWeights {
       }
     }
   }
-  // sum = B v where `here` (v: the lane's chunks of both parts), else as it was
+  // sum = B v where `here` (v: the lane's chunks of all parts), else as it was
   __device__ __forceinline__ void multiply(floatx4 (&sum)[4], const u32x4* v, bool here, int R, int q) const {
     floatx4 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const u32x4 x = here && 4 * k + q < R / 4 ? v[k] : u32x4{0u, 0u, 0u, 0u};
+    for (int k = 0; k < kAll; ++k) {
+      const int step = k < kSteps ? k % kW : k - kSteps;
+      const u32x4 x = here && lora_chunk(k, q, kSteps, R) >= 0 ? v[k] : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = mfma(w[k % kW][i], x, acc[i]);
+      for (int i = 0; i < 4; ++i) acc[i] = mfma(w[step][i], x, acc[i]);
     }
     if (here) {
 #pragma unroll
@@ -359,25 +379,32 @@ __device__ __forceinline__ uint32_t rows_written(int adapter) {
   return (uint32_t)__ballot(mine) & 0xFFFFu;
 }
 
+// Waves per SIMD that the registers have to be enough for. Left to itself the compiler takes 132 with one
+// step, room for three (16384 rows of rank 16 65 us, 49 with four), and 272 with seven, room for one (3000
+// rows of rank 104, both products, 46, 39 with two). The others keep what they have so: eight steps of
+// weights of their own would spill, and rank 128 takes 98 us instead of 92 with its sums moved.
+constexpr int up_waves(int steps) { return steps == 1 ? 4 : steps == 7 ? 2 : 1; }
+
 // `tiles` tiles of 16 rows, one after the other; the adapter's fragments of B stay in registers until
 // a tile has another. Above 64 ranks the workgroup's waves share a tile's v in LDS, loaded two tiles ahead:
 // each for itself, v's bytes are more than those of y and out together (16384 rows into 4096, rank
 // 128: 210 us, shared 179; rank 64 with 8192 rows 77, 82).
 template <int kSteps, bool kHalves, int kWaves, Rows kRows>
-__global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int tiles) {
+__global__ void __launch_bounds__(64 * kWaves, up_waves(kSteps)) lora_up_kernel(LoraProblem p, int tiles) {
   typedef UpRows<kWaves, kRows> Part;
+  typedef UpWeights<kSteps, kHalves> Weights;
   constexpr bool kShared = kSteps > 4;
-  constexpr int kVChunks = 4 * kSteps, kVPitch = 16 * kVChunks + 16;  // (16 rows in distinct banks)
-  constexpr int kVLoads = kShared ? (16 * kVChunks + 64 * kWaves - 1) / (64 * kWaves) : 1;
+  constexpr int kAll = Weights::kAll, kVChunks = lora_tile_chunks(16 * kSteps);  // (at most)
+  constexpr int kVLoads = kShared ? (kVChunks + 64 * kWaves - 1) / (64 * kWaves) : 1;
   __shared__ __align__(16) float sums[2][16 * Part::kPitch];
-  __shared__ __align__(16) uint8_t vs[kShared ? 2 : 1][kShared ? 16 * kVPitch : 16];
+  __shared__ u32x4 vs[kShared ? 2 : 1][kShared ? kVChunks : 1];
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t first = (int64_t)blockIdx.x * (64 * kWaves), n0 = first + 64 * wave;
   const int64_t t0 = (int64_t)blockIdx.y * (16 * tiles);
-  const int R4 = p.R >> 2;  // chunks of a row's v
+  const int64_t last = (p.T - 1) >> 4;  // tile
   struct Tile {
-    u32x4 v[kShared ? 1 : kSteps];
+    u32x4 v[kShared ? 1 : kAll];
     Part rows;
     int adapter;
     uint32_t write;
@@ -387,26 +414,26 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
     k.adapter = adapter_of(p, t);
     k.write = gridDim.z > 1 ? rows_written(k.adapter) : 0xFFFFu;
     if constexpr (!kShared) {
-      const u32x4* v = (const u32x4*)p.down + min(t, p.T - 1) * R4;
+      const u32x4* v = v_tile(p, min((t0 >> 4) + j, last));
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) k.v[i] = v[min(4 * i + q, R4 - 1)];
+      for (int i = 0; i < kAll; ++i) k.v[i] = v_chunk(v, i, kSteps, p.R, q, r);
     }
     k.rows.load(p, t0 + 16 * j, k.write);
   };
-  // a thread's part of a tile's v (past the last rank: the last one's)
+  // a thread's part of a tile's v
   u32x4 part[kVLoads];
   auto load_v = [&](int j) {
 #pragma unroll
     for (int i = 0; i < kVLoads; ++i) {
-      const int at = min(i * 64 * kWaves + (int)threadIdx.x, 16 * kVChunks - 1);
-      part[i] = ((const u32x4*)p.down)[min(t0 + 16 * j + at / kVChunks, p.T - 1) * R4 + min(at % kVChunks, R4 - 1)];
+      const int at = min(i * 64 * kWaves + (int)threadIdx.x, lora_tile_chunks(p.R) - 1);
+      part[i] = v_tile(p, min((t0 >> 4) + j, last))[at];
     }
   };
   auto share_v = [&](int j) {
 #pragma unroll
     for (int i = 0; i < kVLoads; ++i) {
       const int at = i * 64 * kWaves + (int)threadIdx.x;
-      if (at < 16 * kVChunks) *(u32x4*)&vs[j & 1][at / kVChunks * kVPitch + at % kVChunks * 16] = part[i];
+      if (at < lora_tile_chunks(p.R)) vs[j & 1][at] = part[i];
     }
   };
   auto meet = [&]() {
@@ -415,7 +442,7 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
   };
   int held = -1;
-  UpWeights<kSteps, kHalves> w;
+  Weights w;
   Tile now{{}, Part(p, first), -1, 0u}, next{{}, Part(p, first), -1, 0u};
   load(now, 0);
   if (tiles == 1 && now.write == 0) return;  // nothing for this one of a tile's workgroups
@@ -439,9 +466,9 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
       if (a != held) w.load(p, a, n0, q, r);
       held = a;
       if constexpr (kShared) {
-        u32x4 v[kSteps];
+        u32x4 v[kAll];
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) v[k] = *(const u32x4*)&vs[j & 1][r * kVPitch + 16 * (4 * k + q)];
+        for (int k = 0; k < kAll; ++k) v[k] = v_chunk(vs[j & 1], k, kSteps, p.R, q, r);
         w.multiply(sum, v, now.adapter == a, p.R, q);
       } else {
         w.multiply(sum, now.v, now.adapter == a, p.R, q);
@@ -453,7 +480,7 @@ __global__ void __launch_bounds__(64 * kWaves) lora_up_kernel(LoraProblem p, int
     now.rows.store(p, s, t0 + 16 * j, now.write, (uint32_t)__ballot(now.adapter < 0));
     if constexpr (!kShared) {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) now.v[i] = next.v[i];
+      for (int i = 0; i < kAll; ++i) now.v[i] = next.v[i];
     }
     now.rows.y[0] = next.rows.y[0];
     now.rows.y[1] = next.rows.y[1];
@@ -470,9 +497,10 @@ template <int kR, int kC, int kSteps, bool kHalves, Rows kRows>
 __global__ void __launch_bounds__(512) lora_small_kernel(LoraProblem p) {
   constexpr int kWaves = 8, kBytes = kUnitBytes<kR, kC>;
   typedef UpRows<kWaves, kRows> Part;
+  typedef UpWeights<kSteps, kHalves> Weights;
   static_assert(kWaves * kBytes >= 64 * Part::kPitch && kBytes >= kR * 1024, "what follows is held in the same memory");
   __shared__ __align__(16) uint8_t lds[kWaves * kBytes];
-  __shared__ __align__(16) uint16_t parts[16 * 32 * kR];
+  __shared__ u32x4 parts[lora_tile_chunks(16 * kR)];
   const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t first = (int64_t)blockIdx.x * (64 * kWaves), n0 = first + 64 * wave;
@@ -487,7 +515,7 @@ __global__ void __launch_bounds__(512) lora_small_kernel(LoraProblem p) {
   for (int i = 0; i < 4; ++i) sum[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   const __amdgpu_buffer_rsrc_t rx = x_window(p, t0, 16);
   for_adapters(adapter, [&](int a) {
-    UpWeights<kSteps, kHalves> w;
+    Weights w;
     w.load(p, a, n0, q, r);
     const float s = p.scales ? p.scales[a] : 1.0f;
     floatx4 acc[kR];
@@ -499,11 +527,11 @@ __global__ void __launch_bounds__(512) lora_small_kernel(LoraProblem p) {
     for (int i = 0; i < kR; ++i) part[(wave * kR + i) * 64 + lane] = acc[i];
     __syncthreads();
     if (wave < kR && 16 * wave + 4 * q < p.R)
-      store_parts(parts + r * (2 * p.R), 16 * wave + 4 * q, p.R, down_sum<kR, kWaves>(part, wave, lane) * s);
+      store_parts(parts, r, 16 * wave + 4 * q, p.R, down_sum<kR, kWaves>(part, wave, lane) * s);
     __syncthreads();
-    u32x4 v[kSteps];
+    u32x4 v[Weights::kAll];
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) v[k] = *(const u32x4*)&parts[r * (2 * p.R) + 8 * min(4 * k + q, (p.R >> 2) - 1)];
+    for (int k = 0; k < Weights::kAll; ++k) v[k] = v_chunk(parts, k, kSteps, p.R, q, r);
     w.multiply(sum, v, adapter == a, p.R, q);
   });
   __syncthreads();
@@ -545,7 +573,7 @@ void launch_small(const LoraProblem& p, const LoraForm& f, hipStream_t stream) {
 }  // namespace
 
 int64_t lora_down_bytes(int64_t T, int64_t N, int64_t K, int64_t R) {
-  return lora_form(T, N, K, R).down == LoraDown::kFused ? 0 : T * R * 4;
+  return lora_form(T, N, K, R).down == LoraDown::kFused ? 0 : (T + 15) / 16 * lora_tile_chunks((int)R) * 16;
 }
 
 hipError_t launch_lora(const LoraProblem& p, hipStream_t stream) {

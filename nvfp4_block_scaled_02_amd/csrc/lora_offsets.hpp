@@ -11,11 +11,20 @@ namespace {
 // of fragment i are rows 4q .. 4q + 3, columns 16q + 4i .. + 3.
 NVFP4_HD int lora_column(int r, int i) { return 16 * (r >> 2) + 4 * i + (r & 3); }
 
-// The two parts of v along the matrix instruction's K: chunk c (8 elements) of 2R is chunk c % (R / 8) of
-// the upper parts, then of the lower. Whether step k (four chunks) multiplies the same rows of B
-// as step k - R / 32: where R is a multiple of 32.
+// The three parts of v along the matrix instruction's K. Steps (four chunks of 8 elements) of the upper and
+// the middle parts: chunk c of 2R is chunk c % (R / 8) of the upper parts, then of the middle. Whether step
+// k multiplies the same rows of B as step k - R / 32: where R is a multiple of 32. The lower parts begin a
+// step of their own.
 NVFP4_HD bool lora_halves(int R) { return R % 32 == 0; }
 NVFP4_HD int lora_steps(int R) { return (R + 15) / 16; }
+// v of a tile of 16 rows: chunks of [upper R, middle R, lower R], of each chunk all rows. How many times 16 bytes.
+NVFP4_HD constexpr int lora_tile_chunks(int R) { return 3 * (R / 8) * 16; }
+// Chunk that lanes 16 q and on take in step k, `steps` being lora_steps(R); -1: none.
+NVFP4_HD int lora_chunk(int k, int q, int steps, int R) {
+  const int lower = 4 * (k - steps) + q;
+  if (k < steps) return 4 * k + q < R / 4 ? 4 * k + q : -1;
+  return lower < R / 8 ? R / 4 + lower : -1;
+}
 
 // Staging a unit of kC chunks (16 bytes each) of a row: the k-th load of 64 lanes takes rows
 // k * 64 / kC and on, lane l the chunk that its slot l % kC holds of row k * 64 / kC + l / kC. Per-lane

@@ -81,7 +81,7 @@ def lora(y, x, a, b, adapters, scales=None):
     """out [T, N] in float64 before its rounding to bf16, and the tolerance of the rounded one.
 
     v = A x: any order of K fp32 products and sums, relative to the sum of magnitudes (K + 8) u; its
-    scale one rounding more; two bf16 parts: 2^-16 of it. B v: 2R products (each exact: 8 by 8
+    scale one rounding more; its three bf16 parts add up to it. B v: 3R products (each exact: 8 by 8
     bits) and their sums, the addition of y; then half a step of bf16."""
     T, N = y.shape
     L, R, K = a.shape
@@ -93,10 +93,10 @@ def lora(y, x, a, b, adapters, scales=None):
         s = 1.0 if scales is None else float(np.float32(scales[i]))
         A, Bm, X = a[i].astype(np.float64), b[i].astype(np.float64), x[rows].astype(np.float64)
         v, va = s * (X @ A.T), abs(s) * (np.abs(X) @ np.abs(A).T)
-        off = (K + 9) * U * va + 2.0**-16 * np.abs(v)
+        off = (K + 9) * U * va + 2.0**-134
         d, da, do = v @ Bm.T, np.abs(v) @ np.abs(Bm).T, off @ np.abs(Bm).T
         exact = out[rows] + d
-        err = 1.01 * do + (2 * R + 2) * U * 1.01 * (da + np.abs(out[rows]))
+        err = 1.01 * do + (3 * R + 2) * U * 1.01 * (da + np.abs(out[rows]))
         out[rows] = exact
         tol[rows] = err + B * (np.abs(exact) + err)
     return out, tol + 2.0**-133
