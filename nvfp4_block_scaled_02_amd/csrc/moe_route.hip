@@ -347,6 +347,8 @@ __global__ void __launch_bounds__(256) route_rows_kernel(RouteProblem p, int per
     if (lanes > 8) merge(row_lane<0x140>(best), row_lane<0x140>(second));  // row_mirror
     float score = best <= kPlace ? -__builtin_inff() : Key::value(best);
     if (kScored && p.group_best == 2 && second > kPlace) score += Key::value(second);
+    // a sum below what 32 bits hold is not nothing, and may be in another order than others of its like
+    unsure = unsure || (best > kPlace && score == -__builtin_inff());
     int before = 0;
     for (int g = 0; g < p.groups; ++g) {
       const float o = __shfl(score, (lane & 48) + g * lanes, 64);
