@@ -249,7 +249,7 @@ struct Key32 {
 // bits of the place alone.
 //
 // How far such a key is off. Its cut: kPer - 1 last places, with the rounding of the sum with the bias
-// below kPer 2^-22 of its value together (cut; before it, for the groups, 2^-22). A sigmoid s: its
+// below kPer 2^-22 of its value together (cut). A sigmoid s: its
 // exponential's argument is off by at most 2.2 * 2^-24 of itself, which moves s by that times
 // |l| s (1 - s) < 0.23; the hardware's exponential and reciprocal, a last place each (2^-23), move
 // it by s (1 - s) 2^-23 and s 2^-23, the sum between them by s 2^-24: below 2^-22 in all. A share p
@@ -258,6 +258,13 @@ struct Key32 {
 // keys tell their order if they are further apart than cut + 2^-21, or cut + 2^-17 m. Without a
 // bias, where shares may be small, a score is good to 2^-16.8 of itself (arguments up to 68), two
 // are told apart by 2^-15, and none is trusted below 2^-40 m.
+//
+// A group's sum with a bias is off by the roundings of its two keys, 2^-24 of each key's own size, and by its
+// own, 2^-24 of itself: the keys may be of different signs, and their sum far smaller than what it is off
+// by. So each group has an interval of 2^-22 of its keys' sizes together to either side (2^-23, and 2^-24
+// where its end is computed), and the kept groups tell if all of theirs lie above all of the others'. Beside that
+// 2^-21 to either side for two sigmoids, 2^-17 m for two shares (of two groups' difference, at most 2 m, their
+// common factor is 2^-17 m off and the four shares 2^-21 m each).
 template <int kPer, bool kScored, bool kSigmoid>
 __global__ void __launch_bounds__(256) route_rows_kernel(RouteProblem p, int per, bool whole) {
   constexpr uint32_t kPlace = kPer - 1;
@@ -345,19 +352,24 @@ __global__ void __launch_bounds__(256) route_rows_kernel(RouteProblem p, int per
     if (lanes > 2) merge(row_lane<0x4E>(best), row_lane<0x4E>(second));    // quad_perm [2, 3, 0, 1]
     if (lanes > 4) merge(row_lane<0x141>(best), row_lane<0x141>(second));  // row_half_mirror
     if (lanes > 8) merge(row_lane<0x140>(best), row_lane<0x140>(second));  // row_mirror
-    float score = best <= kPlace ? -__builtin_inff() : Key::value(best);
-    if (kScored && p.group_best == 2 && second > kPlace) score += Key::value(second);
-    // a sum below what 32 bits hold is not nothing, and may be in another order than others of its like
-    unsure = unsure || (best > kPlace && score == -__builtin_inff());
+    const bool some = best > kPlace;
+    float score = some ? Key::value(best) : -__builtin_inff(), size = some ? __builtin_fabsf(score) : 0.0f;
+    if (kScored && p.group_best == 2 && second > kPlace) {
+      score += Key::value(second);
+      size += __builtin_fabsf(Key::value(second));
+    }
+    // a sum beyond what 32 bits hold is not nothing, and may be in another order than others of its like
+    unsure = unsure || size == __builtin_inff();
     int before = 0;
     for (int g = 0; g < p.groups; ++g) {
       const float o = __shfl(score, (lane & 48) + g * lanes, 64);
       before += o > score || (o == score && g < group);
     }
     open = before < p.top_groups;
-    // the worst that stays against the best that does not
-    const float in = -row_maxf(open ? -score : -__builtin_inff()), out = row_maxf(open ? -__builtin_inff() : score);
-    if (kScored && out > -__builtin_inff()) unsure = unsure || near(in, out, 2.0f, 0x1p-22f);
+    // the worst that stays against the best that does not, where there are such
+    const float off = kScored && p.bias ? 0x1p-22f * size + (kSigmoid ? 0x1p-21f : 0x1p-17f * most) : 0.0f;
+    const float in = -row_maxf(open ? off - score : -__builtin_inff()), out = row_maxf(open ? -__builtin_inff() : score + off);
+    if (kScored && out > -__builtin_inff()) unsure = unsure || (p.bias ? !(in > out) : near(in, out, 2.0f, 0x1p-22f));
   }
   // v = before - 1 - key of each round; a lane whose group is out has nothing
 #pragma unroll
