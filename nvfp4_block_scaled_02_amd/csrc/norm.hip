@@ -9,8 +9,10 @@
 //
 // Memory-bound: x and y are read and h and out written once (8 bytes per element with a bf16
 // result). A row stays in registers, 8 elements (16 bytes) per thread and chunk, its sums in
-// fp32; mean and variance are taken one after the other, so that a row far from zero loses
-// nothing.
+// fp32. What a sum in fp32 misses of the mean, up to 2^-18 of the values, would stay in every element
+// of a row far from zero: it is what is left of the mean after it is taken away, summed along with the
+// squares. A row of equal values has exactly their mean (its sum, up to 2^15 values of 8 bits, and
+// its quotient are exact), and nothing is left.
 #include "quant_common.hpp"
 #include "quant_mx.hpp"
 #include "wave.hpp"
@@ -23,7 +25,7 @@ namespace {
 // turn: a buffer is written again only behind the next sum's barrier.
 template <int kThreads>
 struct RowSum {
-  float (*part)[kThreads / 64];
+  float (*part)[2 * (kThreads / 64)];
   int turn = 0;
   __device__ __forceinline__ float operator()(float v) {
     v = wave_sum(v);
@@ -36,6 +38,26 @@ struct RowSum {
 #pragma unroll
     for (int w = 1; w < kThreads / 64; ++w) v += p[w];
     return v;
+  }
+  __device__ __forceinline__ void both(float& a, float& b) {
+    constexpr int kWaves = kThreads / 64;
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (kThreads == 64) return;
+    float* p = part[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+      p[threadIdx.x >> 6] = a;
+      p[kWaves + (threadIdx.x >> 6)] = b;
+    }
+    __syncthreads();
+    a = p[0];
+    b = p[kWaves];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      a += p[w];
+      b += p[kWaves + w];
+    }
   }
   __device__ __forceinline__ float max(float v) {  // of values >= 0
     v = u2f(wave_max_u32(f2u(v)));
@@ -54,40 +76,51 @@ struct RowSum {
 // v = norm(v) over the row's H elements, of which this thread holds its chunks.
 template <int kThreads, int kChunks, bool kLayer>
 __device__ __forceinline__ void normalize(float (&v)[kChunks][8], RowSum<kThreads>& sum, int thread, int chunks,
-                                          float rH, float eps) {
+                                          float H, float rH, float eps) {
+  float left = 0.0f, squares = 0.0f;
   if constexpr (kLayer) {
     float s = 0.0f;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += v[c][i];  // (chunks past the row hold zeros)
-    const float mean = sum(s) * rH;
+    const float mean = sum(s) / H;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = thread + kThreads * c < chunks ? v[c][i] - mean : 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        v[c][i] = thread + kThreads * c < chunks ? v[c][i] - mean : 0.0f;
+        left += v[c][i];
+      }
   }
-  float s = 0.0f;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(v[c][i], v[c][i], s);
-  const float r = 1.0f / sqrtf(sum(s) * rH + eps);
+    for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(v[c][i], v[c][i], squares);
+  float off = 0.0f;  // of the mean
+  if constexpr (kLayer) {
+    sum.both(left, squares);
+    off = left * rH;
+    squares = __builtin_fmaxf(__builtin_fmaf(-off, left, squares), 0.0f);  // about the mean
+  } else {
+    squares = sum(squares);
+  }
+  const float r = 1.0f / sqrtf(squares * rH + eps);
 #pragma unroll
   for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[c][i] *= r;
+    for (int i = 0; i < 8; ++i) v[c][i] = (kLayer ? v[c][i] - off : v[c][i]) * r;
 }
 
 // kThreads threads per row (64: four rows per workgroup), kChunks chunks of 8 elements each.
 template <int kThreads, int kChunks, bool kLayer>
 __global__ void __launch_bounds__(kThreads == 64 ? 256 : kThreads) norm_kernel(NormProblem p) {
   constexpr int kRows = kThreads == 64 ? 4 : 1;
-  __shared__ float part[2][kThreads / 64];
+  __shared__ float part[2][2 * (kThreads / 64)];
   RowSum<kThreads> sum{part};
   const int thread = kThreads == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int chunks = (int)(p.H >> 3);
-  const float rH = 1.0f / (float)p.H;
+  const float H = (float)p.H, rH = 1.0f / H;
   const QuantScale qs = p.format == NVFP4_NORM_NVFP4 ? quant_scale(p.gs, 6.0f * p.gs, 1.0f / (6.0f * p.gs), p.gs_dev)
                                                       : QuantScale{1.0f, 6.0f, 1.0f};
   for (int64_t row = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x >> 6 : 0); row < p.M;
@@ -112,7 +145,7 @@ __global__ void __launch_bounds__(kThreads == 64 ? 256 : kThreads) norm_kernel(N
     if (p.y) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) unpack_bf16x8(yv[c], v[c]);
-      if (p.post) normalize<kThreads, kChunks, kLayer>(v, sum, thread, chunks, rH, p.eps);
+      if (p.post) normalize<kThreads, kChunks, kLayer>(v, sum, thread, chunks, H, rH, p.eps);
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const int i = thread + kThreads * c;
@@ -142,7 +175,7 @@ __global__ void __launch_bounds__(kThreads == 64 ? 256 : kThreads) norm_kernel(N
     }
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) unpack_bf16x8(xv[c], v[c]);
-    normalize<kThreads, kChunks, kLayer>(v, sum, thread, chunks, rH, p.eps);
+    normalize<kThreads, kChunks, kLayer>(v, sum, thread, chunks, H, rH, p.eps);
     u32x4 n[kChunks];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {

@@ -109,16 +109,22 @@ _PATH = 64
 
 
 def _norm(v, kind, eps):
-    """norm(v) in float64 and how far the kernel's may be from it."""
+    """norm(v) in float64 and how far the kernel's may be from it.
+
+    Layer: the mean as summed is off by `miss`, _PATH u of the mean magnitude and a rounding. Elements less
+    that mean are rounded once; their own mean takes the miss back but for its sum, _PATH u of the elements'
+    mean magnitude, and three roundings; the elements are rounded once more. The sum of their squares holds the
+    miss's until it is taken off: its _PATH u of both stays."""
     if kind == "layer":
         mean = v.mean(1, keepdims=True)
         d = v - mean
-        off = _PATH * U * np.abs(v).mean(1, keepdims=True) + U * (np.abs(d) + np.abs(mean))
+        miss = (_PATH + 1) * U * np.abs(v).mean(1, keepdims=True)
+        off = (_PATH + 4) * U * (np.abs(d).mean(1, keepdims=True) + miss) + 2 * U * np.abs(d) + U * miss
     else:
-        d, off = v, np.zeros_like(v)
+        d, off, miss = v, np.zeros_like(v), 0.0
     sd = np.sqrt((d * d).mean(1, keepdims=True) + eps)
     n = d / sd
-    worst = off.max(1, keepdims=True) / sd
+    worst = off.max(1, keepdims=True) / sd + _PATH * U * (miss / sd) ** 2
     return n, off / sd + np.abs(n) * (worst + (_PATH / 2 + 8) * U), sd
 
 
