@@ -435,7 +435,9 @@ int nvfp4_lora(const void* y_bf16, const void* x_bf16, const void* a_bf16, const
  * be NULL.
  *   format: out as bf16 [M, H], or that tensor quantized, byte for byte as nvfp4_quantize (under
  *   *global_scale_device, if it is not NULL, or global_scale), nvfp4_mxfp4_quantize,
- *   nvfp4_mxfp8_quantize or nvfp4_fp8r_quantize store it, with its scales.
+ *   nvfp4_mxfp8_quantize or nvfp4_fp8r_quantize store it, with its scales, NaN and infinities among
+ *   them. (NVFP4 has no NaN: a NaN element's code is left open there, the others of its block are as if
+ *   it were zero.)
  *   x_bf16, y_bf16, h_bf16 [M, H]; h may be x. post_weight, weight and bias bf16 [H]; gate, scale and
  *   shift bf16 [groups, H]. rows int32 [M]: each row's group; a row whose group is outside
  *   [0, groups) is not modulated: its scale and shift read as 0, and where there is a gate its h is x.

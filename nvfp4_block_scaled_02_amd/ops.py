@@ -603,7 +603,8 @@ def add_norm(x: torch.Tensor, y: torch.Tensor | None = None, weight: torch.Tenso
 
     ``quantize`` ("nvfp4", "mxfp4", "mxfp8" or "fp8r"): n comes as that format's (codes, scales) pair, byte
     for byte what :func:`quantize` (under ``global_scale``, a float or a device float32 tensor),
-    :func:`mxfp4_quantize`, :func:`mxfp8_quantize` or :func:`fp8r_quantize` make of it."""
+    :func:`mxfp4_quantize`, :func:`mxfp8_quantize` or :func:`fp8r_quantize` make of it (NVFP4 has no NaN: the
+    code of such an element is left open)."""
     dev = _first(x, "x", torch.bfloat16, 2)
     if stream is not None or dev != _current_device():
         with _place(dev, stream):
