@@ -74,9 +74,9 @@ __device__ __forceinline__ Parts three_parts(const floatx4 v) {
 //
 // A workgroup's waves take units of 8 kC elements of K in turn, each for itself. A unit comes through
 // LDS (16 kC consecutive bytes of a row, 64 / kC rows per load): loaded in the matrix instruction's
-// order, every load touches 16 rows (16384 rows of K 4096 and rank 16 57 us instead of 37, 1999 of
-// rank 64 52 instead of 26, both before the parts of a tile's ranks were neighbours). Chunk c (16 bytes) of row s sits at slot c ^ (s % 16), so that the
-// 16 rows of a fragment read are in distinct banks.
+// order, every load touches 16 rows and takes half as long again (16384 rows of K 4096 and rank 16, 34 us
+// as it is) to twice as long (1999 of rank 64, 13). Chunk c (16 bytes) of row s sits at slot
+// c ^ (s % 16), so that the 16 rows of a fragment read are in distinct banks.
 template <int kR, int kC>
 constexpr int kUnitBytes = (1 + kR) * 16 * 16 * kC;
 // acc: this wave's share, of kR fragments of 16 ranks from A's row at w on.
@@ -303,8 +303,8 @@ struct UpWeights {
 //
 // kWhole: N is a multiple of 8, and the loads have no branch around them that would wait for them.
 // kPassing: they leave the caches to v and B, as the stores do; where y is larger than these
-// (both products, 16384 x 4096 of rank 16, 91.7 us, passing 86.0; 8192 x 4096 of rank 64 73.6, 66.5; but
-// 4096 x 2048 20.5, 22.7. With stores that do not pass 96.7, 77.1 and 21.7).
+// (both products, 16384 x 4096 of rank 16, 91.7 us, passing 86.3; 8192 x 4096 of rank 64 72.6, 66.4; but
+// 4096 x 2048 of rank 32 19.9, 22.2).
 enum class Rows { kAny, kWhole, kPassing };
 template <int kWaves, Rows kRows>
 struct UpRows {
@@ -387,8 +387,8 @@ constexpr int up_waves(int steps) { return steps == 1 ? 4 : steps == 7 ? 2 : 1; 
 
 // `tiles` tiles of 16 rows, one after the other; the adapter's fragments of B stay in registers until
 // a tile has another. Above 64 ranks the workgroup's waves share a tile's v in LDS, loaded two tiles ahead:
-// each for itself, v's bytes are more than those of y and out together (16384 rows into 4096, rank
-// 128: 210 us, shared 179; rank 64 with 8192 rows 77, 82).
+// each for itself, v's bytes are more than those of y and out together (both products, 16384 rows into
+// 4096, rank 128: 221 us, shared 161; 3000 of rank 104 93, 39; rank 64 with 8192 rows 66 either way).
 template <int kSteps, bool kHalves, int kWaves, Rows kRows>
 __global__ void __launch_bounds__(64 * kWaves, up_waves(kSteps)) lora_up_kernel(LoraProblem p, int tiles) {
   typedef UpRows<kWaves, kRows> Part;

@@ -64,8 +64,8 @@ NVFP4_HD LoraPart lora_part(uint32_t i, uint32_t n, int R, int ranks) {
 // 64 12.1, 12.5; 600 13.5, 12.3); two above, or for many rows all at once (1999 rows of rank 64 20.1,
 // 18.9, 38.5 for all; 8192 36.7, 35.3, 34.1; 16384 of rank 128 131, 128, 85). Tiles whose adapters are
 // dealt out, up to 1024 workgroups: 48 rows of rank 16 48.7, dealt to 16 11.9. The second product's
-// workgroups: 512, two to a compute unit, of up to 16 tiles each (8192 rows of rank 64 into 4096: 8 tiles
-// 76.9, 12 85.1, 16 74.5, 24 84.5).
+// workgroups: 512, two to a compute unit, of up to 16 tiles each (both products, 8192 rows of rank 64 into
+// 4096: 8 tiles 69.6, 12 76.2, 16 66.4, 24 79.6).
 //
 // The form of the first product: within the second's kernel, with one or two fragments of 16 ranks
 // per tile of rows, or for many rows at once.

@@ -285,8 +285,10 @@ hipError_t launch_add_norm(const NormProblem& p, hipStream_t stream, const Launc
   if (p.M == 0) return hipSuccess;
   const int64_t chunks = p.H >> 3;
   // Threads to a row: as few as hold it in four chunks each, so that many rows are under way (16384 x
-  // 2048: 256 threads 53 us, 512 65; 16384 x 8192 at 5.3 TB/s either way); with no more rows than
-  // compute units one chunk each (64 x 4096: 256 threads 4.5 us, 512 4.0).
+  // 2048: 256 threads 53 us, 512 65; 16384 x 8192 at 5.3 TB/s either way). With no more rows than compute
+  // units, widths of two chunks to 256 threads take one each (64 x 4096: 4.5 us, 512 threads 4.0). Other
+  // widths do not, though they would gain as well (in a graph, 64 x 1024: 3.2 us, 128 threads 2.7; 64 x
+  // 8192: 4.7, 1024 threads 3.7).
   if (chunks > 256 && chunks <= 512 && p.M <= dev.num_cus) return launch<512, 1>(p, stream);
   if (chunks <= 64) return launch<64, 1>(p, stream);
   if (chunks <= 128) return launch<64, 2>(p, stream);
