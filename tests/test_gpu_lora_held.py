@@ -16,6 +16,17 @@ CASES = [  # T, N, K, R: one launch, one or two fragments of ranks per workgroup
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c)))
 def test_last_bits_of_the_first_product(case):
+    _last_bits(case, 0, 0)
+
+
+@pytest.mark.parametrize("case", [(1, 40, 64, 8), (16, 64, 200, 24), (300, 520, 256, 48), (4100, 520, 96, 64)], ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("x_power, a_power", [(-50, -59), (-60, -20), (60, 60)])
+def test_last_bits_of_small_and_large_products(case, x_power, a_power):
+    """The same where v is 2^-109, whose last part is below the least normal bf16, and 2^120."""
+    _last_bits(case, x_power, a_power)
+
+
+def _last_bits(case, x_power, a_power):
     """x of a row holds 1.0 to 1.98, 2^-8 to 2^-7 and 2^-16 to 2^-15 in 8 bits each. Even ranks add all three, 24 bits, and
     odd ones the first two, both exactly in any order; an output column takes p (v_even - v_odd), the third value alone.
     Its six products (three parts each) and y = 0 are added within 2^-24 of at most 2 p each: 8 2^-24 2 p = 2^-20 p. v held
@@ -36,6 +47,8 @@ def test_last_bits_of_the_first_product(case):
     pair = 2 * (n % (R // 2))
     b[0, n, pair], b[0, n, pair + 1] = p, -p
     b[1] = -b[0]
+    # exact powers: v = A x takes 2^(x + a), B takes it back, as far as bf16 goes
+    x, a, b = (np.ldexp(t, e).astype(np.float32) for t, e in ((x, x_power), (a, a_power), (b, -(x_power + a_power))))
     adapters = r.integers(0, 2, T).astype(np.int32)
     x, a, b = (torch.from_numpy(t).cuda().to(torch.bfloat16) for t in (x, a, b))
     y = torch.zeros((T, N), dtype=torch.bfloat16, device="cuda")
